@@ -341,6 +341,65 @@ DSA_API dsa_status indexer_prolog(const dsa_batch* batch, const dsa_prolog_input
                                   uint8_t* q_scale_out, float* w_out, void* k_cache, void* k_scale,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Norm and rotation of queries and keys, with the write of the keys into the
+ * paged cache: what stands between the projections and the attention of this
+ * library (the prolog above makes indexer inputs and does not rotate).
+ * For each query head x = q[t, h, :] and each token's key x = k[t, :] of D
+ * elements (an MLA row: 512 latent + 64 RoPE; an indexer row: D_I):
+ *     y_i = x_i * gamma_i / sqrt(mean_{j < n} x_j^2 + eps)    for i < n
+ *     y_i = x_i                                               for i >= n
+ * with n = q_norm or k_norm (0: no norm), then the elements
+ * [rope_off, rope_off + rope_dim) are rotated in pairs by the angles
+ * pos * inv_freq[i]: (a, b) -> (a cos - b sin, b cos + a sin), pairs being
+ * (i, i + rope_dim/2), or (2i, 2i + 1) when interleaved.  pos is positions[t],
+ * or the token's place in its sequence when positions is NULL.  The angle is
+ * formed in 64 bits, statistics and products in 32; each result is rounded
+ * once.
+ * q_out [T, H, D] bf16, dense; it may be q itself when q is dense, and must not
+ * overlap q otherwise.  k goes to the cache row of the token's place in its
+ * sequence (seq_lens[b] - nq_b + j, page from the block table): bf16 rows
+ * [num_blocks, 64, D], or with kv_dtype DSA_KV_FP8 (D = 576 only) e4m3fn codes
+ * plus k_scale [num_blocks, 64, 5], scale amax/448 of each 128 elements (1
+ * where that is zero), codes rounded to nearest even, a zero stored as +0.  No
+ * other cache row is touched.  Two tokens must not share a cache row.
+ * Rows of q_out behind the last sequence (t >= cu_q[B], a padded batch) are
+ * left as they were.  A key whose page id or position is out of range is
+ * skipped and recorded as DSA_ERR_DEVICE_BOUNDS.
+ * q may be NULL (keys only), and k may be NULL (queries only; block_table is
+ * not read then).  batch->max_seq_len and max_q_per_seq are not used.
+ */
+typedef struct {
+    const void* q;              /* device [T, H, D] bf16, 16-byte aligned, or NULL                          */
+    int64_t q_stride_t;         /* elements from one token (head) of q to the next: multiples of 8, >= 0    */
+    int64_t q_stride_h;
+    const void* k;              /* device [T, D] bf16, 16-byte aligned, or NULL                             */
+    int64_t k_stride_t;         /* elements from one token of k to the next: a multiple of 8, >= 0          */
+    int32_t H;                  /* query heads, >= 1                                                        */
+    int32_t D;                  /* elements per row: a multiple of 8, up to 1024                            */
+    const float* q_gamma;       /* device [q_norm] fp32, 16-byte aligned (NULL when q_norm is 0)            */
+    const float* k_gamma;       /* device [k_norm] fp32, 16-byte aligned (NULL when k_norm is 0)            */
+    int32_t q_norm;             /* leading elements that are normalized: a multiple of 8, 0..D              */
+    int32_t k_norm;
+    float eps;                  /* >= 0                                                                     */
+    const float* inv_freq;      /* device [rope_dim / 2] fp32 angles per position (NULL when rope_dim is 0) */
+    int32_t rope_dim;           /* rotated elements: a multiple of 16 (0: none)                             */
+    int32_t rope_off;           /* first rotated element: a multiple of 8                                   */
+    int32_t interleaved;        /* 0: pairs (i, i + rope_dim/2); 1: pairs (2i, 2i + 1)                      */
+    const int32_t* positions;   /* device [T] rotation positions, or NULL                                   */
+    int32_t kv_dtype;           /* dsa_kv_dtype of the cache that k is written to                           */
+} dsa_rope_inputs;
+
+/*
+ * One launch.  status is a status area (256 bytes, zero-filled before its
+ * first use; the start of any workspace of this library serves) that
+ * dsa_get_status reads; it may be NULL when k is NULL.  No workspace is used.
+ * Returns DSA_ERR_INVALID_ARG / DSA_ERR_UNSUPPORTED before launching anything,
+ * DSA_ERR_CUDA if the launch fails.
+ */
+DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_inputs* in, void* q_out, void* k_cache,
+                                    float* k_scale, void* status, void* stream);
+
 /* Static description of a status code. */
 DSA_API const char* dsa_status_str(int32_t status);
 

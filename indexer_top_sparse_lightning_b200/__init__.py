@@ -16,6 +16,8 @@ Entry points (same names as the C ABI):
     indexer_prolog(batch, x, w_proj, k_gamma, eps, k_cache, k_scale=None, mx=False)
         -> (q_idx, q_scale or None, w)   (also writes the tokens' keys into k_cache / k_scale;
         w_proj row-major, or prolog_pack_weights(w_proj, H_I, D_I) for weight streaming)
+    dsa_qk_norm_rope(batch, inv_freq, q, k, q_gamma=None, k_gamma=None, k_cache=None, ...) -> q_out
+        (per-head norm and rotation of queries and keys; keys go into the paged cache)
 
 Key formats: bf16 keys (k_scale None); e4m3 keys (uint8) with fp32 k_scale
 [nblk, 64, D_I/64]; MXFP8 queries and keys when q_scale is given: q_idx and
@@ -29,8 +31,10 @@ import os
 from dataclasses import dataclass
 from typing import Optional
 
+import torch
+
 __all__ = ["Batch", "Workspace", "indexer_topk", "sparse_mla_attn", "dsa_decode", "indexer_prolog",
-           "prolog_pack_weights", "PackedWeights", "get_status",
+           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "get_status", "status_workspace",
            "DsaError", "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -84,6 +88,15 @@ class _Prolog(ctypes.Structure):
                 ("w_layout", ctypes.c_int32)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("k_stride_t", ctypes.c_int64), ("H", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p),
+                ("q_norm", ctypes.c_int32), ("k_norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p), ("rope_dim", ctypes.c_int32), ("rope_off", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p), ("kv_dtype", ctypes.c_int32)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -128,6 +141,9 @@ def load_library():
     lib.indexer_prolog_pack.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_void_p]
     lib.indexer_prolog_pack.restype = ctypes.c_int
+    lib.dsa_qk_norm_rope.argtypes = [P(_Batch), P(_Rope), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p]
+    lib.dsa_qk_norm_rope.restype = ctypes.c_int
     lib.dsa_status_str.argtypes = [ctypes.c_int32]
     lib.dsa_status_str.restype = ctypes.c_char_p
     lib.dsa_version.restype = ctypes.c_char_p
@@ -150,13 +166,11 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> int:
-    import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return int(s.cuda_stream)
 
 
 def _check(t, name, dtype, ndim=None, shape=None):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -186,7 +200,6 @@ class Batch:
 
     @classmethod
     def from_tensors(cls, seq_lens, cu_q, block_table, num_blocks, max_seq_len=None, max_q_per_seq=None):
-        import torch
         for t, n in ((seq_lens, "seq_lens"), (cu_q, "cu_q"), (block_table, "block_table")):
             _check(t, n, torch.int32)
         if max_seq_len is None:
@@ -205,7 +218,6 @@ class Batch:
 
 
 def _indexer_struct(q_idx, w, k_cache, k_scale, K, q_scale=None):
-    import torch
     if q_scale is not None:
         # MXFP8 queries and keys
         _check(q_idx, "q_idx", torch.uint8, 3)
@@ -233,7 +245,6 @@ def _indexer_struct(q_idx, w, k_cache, k_scale, K, q_scale=None):
 
 
 def _attn_struct(q, kv_cache, sm_scale, kv_scale=None):
-    import torch
     _check(q, "q", torch.bfloat16, 3, (None, None, 576))
     if kv_scale is None:
         _check(kv_cache, "kv_cache", torch.bfloat16, 3, (None, 64, 576))
@@ -251,12 +262,10 @@ class Workspace:
     kernels leave it zero-filled after every successful call."""
 
     def __init__(self, device=None):
-        import torch
         self.device = torch.device("cuda") if device is None else torch.device(device)
         self.buf = None
 
     def get(self, nbytes: int):
-        import torch
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
         return self.buf
@@ -270,7 +279,6 @@ _default_ws = {}
 
 
 def _workspace(ws, device):
-    import torch
     if ws is not None:
         return ws
     device = torch.device(device)
@@ -283,7 +291,6 @@ def _workspace(ws, device):
 def indexer_topk(batch: Batch, q_idx, w, k_cache, K: int, k_scale=None, q_scale=None, *, out_idx=None, out_score=None,
                  want_score: bool = True, workspace: Optional[Workspace] = None, stream=None):
     """Fused Lightning Indexer + Top-K.  Returns (idx [T,K] int32, score [T,K] fp32 or None)."""
-    import torch
     lib = load_library()
     ix, T = _indexer_struct(q_idx, w, k_cache, k_scale, K, q_scale)
     cb = batch.c(T)
@@ -307,7 +314,6 @@ def sparse_mla_attn(batch: Batch, q, kv_cache, idx, sm_scale: float, *, kv_scale
                     want_lse: bool = True, workspace: Optional[Workspace] = None, stream=None):
     """Sparse Flash Attention over the selected latent rows (bf16 cache, or an FP8 cache of e4m3
     codes with kv_scale).  Returns (out [T,H,512] bf16, lse [T,H] fp32)."""
-    import torch
     lib = load_library()
     at, T = _attn_struct(q, kv_cache, sm_scale, kv_scale)
     _check(idx, "idx", torch.int32, 2, (T, None))
@@ -333,7 +339,6 @@ def sparse_mla_attn_static(batch: Batch, q, kv_cache, idx, sm_scale: float, *, o
                            want_lse: bool = True, stream=None):
     """sparse_mla_attn without a workspace: the library's fixed scratch is used
     (calls on one device must not overlap).  Returns (out, lse)."""
-    import torch
     lib = load_library()
     at, T = _attn_struct(q, kv_cache, sm_scale)
     _check(idx, "idx", torch.int32, 2, (T, None))
@@ -355,7 +360,6 @@ def dsa_decode(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm_scale: f
                workspace: Optional[Workspace] = None, stream=None):
     """Whole step (indexer + Top-K + sparse attention) on one stream.
     Returns (idx, score or None, out, lse or None)."""
-    import torch
     lib = load_library()
     ix, T = _indexer_struct(q_idx, w, k_cache, k_scale, K, q_scale)
     at, T2 = _attn_struct(q, kv_cache, sm_scale, kv_scale)
@@ -389,7 +393,6 @@ _prolog_ws = {}
 def prolog_workspace(device=None) -> Workspace:
     """The default workspace of indexer_prolog on a device (kept apart from the
     other entry points' workspace: its partial-tile region is scratch)."""
-    import torch
     device = torch.device("cuda") if device is None else torch.device(device)
     key = device.index if device.index is not None else torch.cuda.current_device()
     if key not in _prolog_ws:
@@ -407,7 +410,6 @@ class PackedWeights:
 def prolog_pack_weights(w_proj, H_I: int, D_I: int, stream=None) -> PackedWeights:
     """Tile-packed copy of the row-major prolog weights w_proj [H_I*D_I + D_I + H_I, d] (bf16):
     each 128-row x 64-column block contiguous (done once, when the weights are loaded)."""
-    import torch
     lib = load_library()
     _check(w_proj, "w_proj", torch.bfloat16, 2, (H_I * D_I + D_I + H_I, None))
     d = int(w_proj.shape[1])
@@ -429,7 +431,6 @@ def indexer_prolog(batch: Batch, x, w_proj, k_gamma, eps: float, k_cache, k_scal
     eps) and writes them into the tokens' rows of the paged key cache (format given by
     k_cache / k_scale as for indexer_topk; MXFP8 when mx).  Returns (q_idx [T, H_I, D_I]
     bf16 or e4m3 codes, q_scale [T, H_I, D_I/32] uint8 or None, w [T, H_I] fp32)."""
-    import torch
     lib = load_library()
     _check(x, "x", torch.bfloat16, 2)
     _check(k_gamma, "k_gamma", torch.float32, 1)
@@ -480,6 +481,142 @@ def indexer_prolog(batch: Batch, x, w_proj, k_gamma, eps: float, k_cache, k_scal
     return q_out, q_scale_out, w_out
 
 
+_status_ws = {}
+
+
+def status_workspace(device=None) -> Workspace:
+    """The default status area of dsa_qk_norm_rope on a
+    device: read it with get_status(status_workspace(device)).  It keeps its address for
+    the life of the process, so captured graphs may hold it."""
+    device = torch.device("cuda") if device is None else torch.device(device)
+    key = device.index if device.index is not None else torch.cuda.current_device()
+    if key not in _status_ws:
+        ws = Workspace(torch.device("cuda", key))
+        ws.get(256)
+        # zeroed before any stream can use it
+        torch.cuda.synchronize(ws.device)
+        _status_ws[key] = ws
+    return _status_ws[key]
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream (the device's current one
+    by default), so that outputs and scratch are allocated for the stream that uses them."""
+
+    def __init__(self, device, stream):
+        self.dev = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return _stream(None)
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.dev.__exit__(*exc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the queries on {device}")
+
+
+def _check_batch(batch: Batch, device, T: int):
+    _check(batch.seq_lens, "seq_lens", torch.int32, 1)
+    B = batch.B
+    _check(batch.cu_q, "cu_q", torch.int32, 1, (B + 1,))
+    _check(batch.block_table, "block_table", torch.int32, 2, (B, None))
+    _same_device(device, seq_lens=batch.seq_lens, cu_q=batch.cu_q, block_table=batch.block_table)
+    return batch.c(T)
+
+
+def _check_rows(t, name, ndim):
+    """A bf16 CUDA tensor whose last dimension is dense and whose other strides keep 16-byte rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    # the stride of a dimension of one element is never used
+    strides = [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]
+    if (t.shape[-1] > 1 and strides[-1] != 1) or any(s % 8 for s in strides[:-1]) or t.data_ptr() % 16:
+        raise ValueError(f"{name} needs dense, 16-byte aligned rows, got strides {t.stride()}")
+    return strides
+
+
+def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_gamma=None, eps: float = 1e-6,
+                     rope_off: Optional[int] = None, interleaved: bool = False, positions=None, k_cache=None,
+                     k_scale=None, q_out=None, workspace: Optional[Workspace] = None, stream=None):
+    """Per-head RMS norm and position rotation of the step's queries q [T, H, D] and keys
+    k [T, D] (bf16, rows may be strided) in one pass; the keys go into the tokens' rows of
+    k_cache (bf16 [nblk, 64, D], or uint8 e4m3 codes of 576-element latent rows with k_scale
+    [nblk, 64, 5]).  q_gamma / k_gamma (fp32) normalize as many leading elements as they
+    have; inv_freq (fp32, or None) rotates twice its length from rope_off on (the row's end
+    by default) by the tokens' places in their sequences, or by positions [T] int32.
+    Returns q_out [T, H, D] (which may be q itself), or None without q."""
+    lib = load_library()
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    s = _Rope()
+    main = q if q is not None else k
+    if q is not None:
+        qs = _check_rows(q, "q", 3)
+        T, s.H, s.D = (int(n) for n in q.shape)
+        s.q, s.q_stride_t, s.q_stride_h = _ptr(q), qs[0], qs[1]
+    if k is not None:
+        ks = _check_rows(k, "k", 2)
+        if q is not None and (k.shape[0] != T or k.shape[1] != s.D):
+            raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
+        T, s.D = (int(n) for n in k.shape)
+        s.k, s.k_stride_t = _ptr(k), ks[0]
+        if k_scale is None:
+            _check(k_cache, "k_cache", torch.bfloat16, 3, (batch.num_blocks, 64, s.D))
+            s.kv_dtype = KV_BF16
+        else:
+            _check(k_cache, "k_cache", torch.uint8, 3, (batch.num_blocks, 64, s.D))
+            _check(k_scale, "k_scale", torch.float32, 3, (batch.num_blocks, 64, 5))
+            s.kv_dtype = KV_FP8
+    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+        if g is not None:
+            _check(g, name, torch.float32, 1)
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32, 1)
+        s.rope_dim = 2 * int(inv_freq.shape[0])
+    if positions is not None:
+        _check(positions, "positions", torch.int32, 1, (T,))
+    dev = main.device
+    _same_device(dev, k=k, q_gamma=q_gamma, k_gamma=k_gamma, inv_freq=inv_freq, positions=positions,
+                 k_cache=k_cache, k_scale=k_scale, q_out=q_out)
+    cb = _check_batch(batch, dev, T)
+    s.rope_off = s.D - s.rope_dim if rope_off is None else int(rope_off)
+    s.interleaved = int(bool(interleaved))
+    s.eps = float(eps)
+    s.q_gamma, s.q_norm = _ptr(q_gamma), 0 if q_gamma is None else int(q_gamma.shape[0])
+    s.k_gamma, s.k_norm = _ptr(k_gamma), 0 if k_gamma is None else int(k_gamma.shape[0])
+    s.inv_freq, s.positions = _ptr(inv_freq), _ptr(positions)
+    status = (workspace if workspace is not None else status_workspace(dev)).get(256)
+    with _On(dev, stream) as on:
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((T, s.H, s.D), dtype=torch.bfloat16, device=dev)
+            else:
+                _check(q_out, "q_out", torch.bfloat16, 3, (T, s.H, s.D))
+                if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+                    raise ValueError("q_out may be q only when q is contiguous")
+        rc = lib.dsa_qk_norm_rope(ctypes.byref(cb), ctypes.byref(s), _ptr(q_out) if q is not None else None,
+                                  _ptr(k_cache), _ptr(k_scale), _ptr(status), on)
+    if rc != 0:
+        raise DsaError(rc, "dsa_qk_norm_rope")
+    return q_out
+
+
 def decode_launch_count(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm_scale: float,
                         k_scale=None, q_scale=None, kv_scale=None) -> int:
     """Kernel launches one dsa_decode call enqueues for these shapes."""
@@ -495,7 +632,6 @@ def decode_launch_count(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm
 
 def get_status(workspace: Optional[Workspace] = None, device=None, stream=None) -> int:
     """Synchronize and read (and clear) the device status word of a workspace."""
-    import torch
     lib = load_library()
     ws = _workspace(workspace, device if device is not None else torch.device("cuda"))
     buf = ws.get(256)
