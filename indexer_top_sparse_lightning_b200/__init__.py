@@ -488,8 +488,9 @@ def status_workspace(device=None) -> Workspace:
     """The default status area of dsa_qk_norm_rope on a
     device: read it with get_status(status_workspace(device)).  It keeps its address for
     the life of the process, so captured graphs may hold it."""
-    device = torch.device("cuda") if device is None else torch.device(device)
-    key = device.index if device.index is not None else torch.cuda.current_device()
+    key = None if device is None else torch.device(device).index
+    if key is None:
+        key = torch.cuda.current_device()
     if key not in _status_ws:
         ws = Workspace(torch.device("cuda", key))
         ws.get(256)
@@ -500,55 +501,80 @@ def status_workspace(device=None) -> Workspace:
 
 
 class _On:
-    """The device of a call's tensors made current, and its stream (the device's current one
-    by default), so that outputs and scratch are allocated for the stream that uses them."""
+    """The device of a call's tensors (by index) made current, and its stream (the device's
+    current one by default), so that outputs and scratch are allocated for the stream that
+    uses them.  Entering it gives the stream's handle."""
+    __slots__ = ("dev", "stream", "left")
 
-    def __init__(self, device, stream):
-        self.dev = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream) if stream is not None else None
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream, self.left = dev, stream, ()
 
     def __enter__(self):
-        self.dev.__enter__()
         if self.stream is not None:
-            self.stream.__enter__()
-        return _stream(None)
+            if self.stream.device.index != self.dev:
+                raise ValueError(f"the stream is on {self.stream.device}, the tensors on cuda:{self.dev}")
+            self.left = (torch.cuda.device(self.dev), torch.cuda.stream(self.stream))
+        elif torch._C._cuda_getDevice() != self.dev:
+            self.left = (torch.cuda.device(self.dev),)
+        for c in self.left:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.dev)
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.dev.__exit__(*exc)
+        for c in reversed(self.left):
+            c.__exit__(*exc)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the queries on {device}")
+def _dense(t, name, dtype, shape, dev: int) -> int:
+    """Pointer of a dense tensor of this type, shape and device index; raises what is wrong with another."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, len(shape), shape)
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
 
 
-def _check_batch(batch: Batch, device, T: int):
-    _check(batch.seq_lens, "seq_lens", torch.int32, 1)
-    B = batch.B
-    _check(batch.cu_q, "cu_q", torch.int32, 1, (B + 1,))
-    _check(batch.block_table, "block_table", torch.int32, 2, (B, None))
-    _same_device(device, seq_lens=batch.seq_lens, cu_q=batch.cu_q, block_table=batch.block_table)
-    return batch.c(T)
+def _vector(t, name, dtype, dev: int):
+    """(pointer, length) of a dense vector, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    n = t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 1 else None
+    return _dense(t, name, dtype, (n,), dev), n
 
 
-def _check_rows(t, name, ndim):
-    """A bf16 CUDA tensor whose last dimension is dense and whose other strides keep 16-byte rows."""
+def _batch_struct(batch: Batch, T: int, dev: int) -> _Batch:
+    """The batch's argument block, its tensors checked."""
+    t = batch.seq_lens
+    B = t.shape[0] if t.dim() == 1 else None
+    table = batch.block_table
+    W = table.shape[1] if table.dim() == 2 else None
+    i32 = torch.int32
+    return _Batch(B, T, _dense(t, "seq_lens", i32, (B,), dev), _dense(batch.cu_q, "cu_q", i32, (B + 1,), dev),
+                  _dense(table, "block_table", i32, (B, W), dev), W, batch.num_blocks, batch.max_seq_len,
+                  batch.max_q_per_seq)
+
+
+def _rows(t, name, ndim: int, dev: int):
+    """Shape and strides of a bf16 CUDA tensor of dense, 16-byte aligned rows (other strides may be any)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    # the stride of a dimension of one element is never used
-    strides = [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]
-    if (t.shape[-1] > 1 and strides[-1] != 1) or any(s % 8 for s in strides[:-1]) or t.data_ptr() % 16:
-        raise ValueError(f"{name} needs dense, 16-byte aligned rows, got strides {t.stride()}")
-    return strides
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(shape)}")
+    if not t.is_contiguous():
+        # the stride of a dimension of one element is never used
+        strides = [s if n > 1 else 0 for n, s in zip(shape, strides)]
+        if (shape[-1] > 1 and strides[-1] != 1) or any(s % 8 for s in strides[:-1]):
+            raise ValueError(f"{name} needs dense rows 16 bytes apart, got strides {t.stride()}")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    return shape, strides
 
 
 def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_gamma=None, eps: float = 1e-6,
@@ -562,59 +588,49 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
     by default) by the tokens' places in their sequences, or by positions [T] int32.
     Returns q_out [T, H, D] (which may be q itself), or None without q."""
     lib = load_library()
-    if q is None and k is None:
-        raise ValueError("q or k is needed")
-    s = _Rope()
     main = q if q is not None else k
+    if main is None:
+        raise ValueError("q or k is needed")
+    dev = main.get_device() if isinstance(main, torch.Tensor) else -1
+    f32 = torch.float32
+    H = qp = kp = cp = sp = 0
+    qs, ks, kt = (0, 0), (0,), KV_BF16
     if q is not None:
-        qs = _check_rows(q, "q", 3)
-        T, s.H, s.D = (int(n) for n in q.shape)
-        s.q, s.q_stride_t, s.q_stride_h = _ptr(q), qs[0], qs[1]
+        (T, H, D), qs = _rows(q, "q", 3, dev)
+        qp = q.data_ptr()
     if k is not None:
-        ks = _check_rows(k, "k", 2)
-        if q is not None and (k.shape[0] != T or k.shape[1] != s.D):
-            raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
-        T, s.D = (int(n) for n in k.shape)
-        s.k, s.k_stride_t = _ptr(k), ks[0]
+        shape, ks = _rows(k, "k", 2, dev)
+        if q is not None and shape != (T, D):
+            raise ValueError(f"k {tuple(shape)} does not match q {tuple(q.shape)}")
+        T, D = shape
+        kp = k.data_ptr()
         if k_scale is None:
-            _check(k_cache, "k_cache", torch.bfloat16, 3, (batch.num_blocks, 64, s.D))
-            s.kv_dtype = KV_BF16
+            cp = _dense(k_cache, "k_cache", torch.bfloat16, (batch.num_blocks, 64, D), dev)
         else:
-            _check(k_cache, "k_cache", torch.uint8, 3, (batch.num_blocks, 64, s.D))
-            _check(k_scale, "k_scale", torch.float32, 3, (batch.num_blocks, 64, 5))
-            s.kv_dtype = KV_FP8
-    for g, name in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
-        if g is not None:
-            _check(g, name, torch.float32, 1)
-    if inv_freq is not None:
-        _check(inv_freq, "inv_freq", torch.float32, 1)
-        s.rope_dim = 2 * int(inv_freq.shape[0])
-    if positions is not None:
-        _check(positions, "positions", torch.int32, 1, (T,))
-    dev = main.device
-    _same_device(dev, k=k, q_gamma=q_gamma, k_gamma=k_gamma, inv_freq=inv_freq, positions=positions,
-                 k_cache=k_cache, k_scale=k_scale, q_out=q_out)
-    cb = _check_batch(batch, dev, T)
-    s.rope_off = s.D - s.rope_dim if rope_off is None else int(rope_off)
-    s.interleaved = int(bool(interleaved))
-    s.eps = float(eps)
-    s.q_gamma, s.q_norm = _ptr(q_gamma), 0 if q_gamma is None else int(q_gamma.shape[0])
-    s.k_gamma, s.k_norm = _ptr(k_gamma), 0 if k_gamma is None else int(k_gamma.shape[0])
-    s.inv_freq, s.positions = _ptr(inv_freq), _ptr(positions)
-    status = (workspace if workspace is not None else status_workspace(dev)).get(256)
+            kt = KV_FP8
+            cp = _dense(k_cache, "k_cache", torch.uint8, (batch.num_blocks, 64, D), dev)
+            sp = _dense(k_scale, "k_scale", f32, (batch.num_blocks, 64, 5), dev)
+    qg, qn = _vector(q_gamma, "q_gamma", f32, dev)
+    kg, kn = _vector(k_gamma, "k_gamma", f32, dev)
+    fp, R = _vector(inv_freq, "inv_freq", f32, dev)
+    R *= 2
+    pp = None if positions is None else _dense(positions, "positions", torch.int32, (T,), dev)
+    cb = _batch_struct(batch, T, dev)
+    s = _Rope(qp, qs[0], qs[1], kp, ks[0], H, D, qg, kg, qn, kn, eps, fp, R,
+              D - R if rope_off is None else rope_off, bool(interleaved), pp, kt)
+    status = _ptr((workspace if workspace is not None else status_workspace(main.device)).get(256))
     with _On(dev, stream) as on:
+        op = 0
         if q is not None:
             if q_out is None:
-                q_out = torch.empty((T, s.H, s.D), dtype=torch.bfloat16, device=dev)
-            else:
-                _check(q_out, "q_out", torch.bfloat16, 3, (T, s.H, s.D))
-                if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
-                    raise ValueError("q_out may be q only when q is contiguous")
-        rc = lib.dsa_qk_norm_rope(ctypes.byref(cb), ctypes.byref(s), _ptr(q_out) if q is not None else None,
-                                  _ptr(k_cache), _ptr(k_scale), _ptr(status), on)
+                q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=main.device)
+            op = _dense(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
+            if op == qp and not q.is_contiguous():
+                raise ValueError("q_out may be q only when q is contiguous")
+        rc = lib.dsa_qk_norm_rope(ctypes.byref(cb), ctypes.byref(s), op, cp, sp, status, on)
     if rc != 0:
         raise DsaError(rc, "dsa_qk_norm_rope")
-    return q_out
+    return q_out if q is not None else None
 
 
 def decode_launch_count(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm_scale: float,
