@@ -158,7 +158,8 @@ typedef struct {
  * many microseconds (0 = the default of one second), word 2 injects a wait
  * that runs out (bit 0: an indexer group barrier waits for one CTA more than
  * its group has; bit 1: in the attention kernel the second CTA of each pair
- * never reports its first rows).
+ * never reports its first rows; bit 2: in dsa_chunk_attn the second CTA of each
+ * pair never loads).
  * Returns 0 if the shape is invalid.
  */
 DSA_API size_t dsa_workspace_size(const dsa_batch* batch, const dsa_indexer_inputs* ix,
@@ -399,6 +400,39 @@ typedef struct {
  */
 DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_inputs* in, void* q_out, void* k_cache,
                                     float* k_scale, void* status, void* stream);
+
+/*
+ * Dense attention of new tokens over the paged latent cache: every query token
+ * attends to all positions up to its own (chunks of a prompt, single tokens,
+ * tokens to verify; layers and contexts that stay dense beside the sparse
+ * attention above).  With p_t = seq_lens[b] - nq_b + j the position of token j
+ * of sequence b (its latent row and the ones before it are in the cache):
+ *     S[t,h,s] = sm_scale * q[t,h,:] . row_s[0:576]     for s = 0..p_t
+ *     out[t,h,:] = sum_s softmax(S[t,h,:])_s row_s[0:512]
+ *     lse[t,h] = log sum_s exp(S[t,h,s])
+ * q, cache formats and block tables are those of sparse_mla_attn; an FP8 cache
+ * is dequantized once per call into the scratch (bf16, rounded once), which
+ * then holds max_seq_len rows for each sequence.
+ * out device [T, H, 512] bf16; lse device [T, H] fp32 (natural log) or NULL.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to
+ * bf16 for the second product.
+ * Rows of the cache at positions that a token does not see may hold anything,
+ * and do not reach its result.  Rows of out and lse behind the last sequence
+ * (t >= cu_q[B]) are left as they were.  Sequences without new tokens are
+ * allowed.  A page id out of range, or lengths that do not fit the table, are
+ * recorded as DSA_ERR_DEVICE_BOUNDS; the positions of such a page are not seen.
+ *
+ * status: a status area (256 bytes, zero-filled before its first use; the start
+ * of any workspace of this library serves), read by dsa_get_status; calls may
+ * share one.  scratch: dsa_chunk_scratch_size bytes, 256-byte aligned, of any
+ * contents; it is in use until the call's work completes, and calls that may
+ * overlap in time need one each.  Returns DSA_ERR_INVALID_ARG /
+ * DSA_ERR_UNSUPPORTED / DSA_ERR_WORKSPACE before launching anything,
+ * DSA_ERR_CUDA if a launch fails.
+ */
+DSA_API size_t dsa_chunk_scratch_size(const dsa_batch* batch, const dsa_attn_inputs* at);
+DSA_API dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, void* out, float* lse,
+                                  void* status, void* scratch, size_t scratch_bytes, void* stream);
 
 /* Static description of a status code. */
 DSA_API const char* dsa_status_str(int32_t status);

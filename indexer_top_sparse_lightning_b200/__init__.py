@@ -18,6 +18,8 @@ Entry points (same names as the C ABI):
         w_proj row-major, or prolog_pack_weights(w_proj, H_I, D_I) for weight streaming)
     dsa_qk_norm_rope(batch, inv_freq, q, k, q_gamma=None, k_gamma=None, k_cache=None, ...) -> q_out
         (per-head norm and rotation of queries and keys; keys go into the paged cache)
+    dsa_chunk_attn(batch, q, kv_cache, sm_scale, kv_scale=None) -> (out, lse)
+        (dense causal attention of the new tokens over the paged latent cache)
 
 Key formats: bf16 keys (k_scale None); e4m3 keys (uint8) with fp32 k_scale
 [nblk, 64, D_I/64]; MXFP8 queries and keys when q_scale is given: q_idx and
@@ -34,7 +36,7 @@ from typing import Optional
 import torch
 
 __all__ = ["Batch", "Workspace", "indexer_topk", "sparse_mla_attn", "dsa_decode", "indexer_prolog",
-           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "get_status", "status_workspace",
+           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "dsa_chunk_attn", "get_status", "status_workspace",
            "DsaError", "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -144,6 +146,11 @@ def load_library():
     lib.dsa_qk_norm_rope.argtypes = [P(_Batch), P(_Rope), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_void_p]
     lib.dsa_qk_norm_rope.restype = ctypes.c_int
+    lib.dsa_chunk_scratch_size.argtypes = [P(_Batch), P(_Attn)]
+    lib.dsa_chunk_scratch_size.restype = ctypes.c_size_t
+    lib.dsa_chunk_attn.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                   ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.dsa_chunk_attn.restype = ctypes.c_int
     lib.dsa_status_str.argtypes = [ctypes.c_int32]
     lib.dsa_status_str.restype = ctypes.c_char_p
     lib.dsa_version.restype = ctypes.c_char_p
@@ -485,7 +492,7 @@ _status_ws = {}
 
 
 def status_workspace(device=None) -> Workspace:
-    """The default status area of dsa_qk_norm_rope on a
+    """The default status area of dsa_qk_norm_rope and dsa_chunk_attn on a
     device: read it with get_status(status_workspace(device)).  It keeps its address for
     the life of the process, so captured graphs may hold it."""
     key = None if device is None else torch.device(device).index
@@ -631,6 +638,49 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
     if rc != 0:
         raise DsaError(rc, "dsa_qk_norm_rope")
     return q_out if q is not None else None
+
+
+def _latent_attn(q, kv_cache, sm_scale, kv_scale, num_blocks: int):
+    """(argument block, T, H, device index) of dense queries and the latent cache they attend to."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _check(q, "q", torch.bfloat16, 3)
+    T, H, _ = q.shape
+    dev = q.get_device()
+    qp = _dense(q, "q", torch.bfloat16, (T, H, 576), dev)
+    if kv_scale is None:
+        kt, sp = KV_BF16, None
+        cp = _dense(kv_cache, "kv_cache", torch.bfloat16, (num_blocks, 64, 576), dev)
+    else:
+        kt, sp = KV_FP8, _dense(kv_scale, "kv_scale", torch.float32, (num_blocks, 64, 5), dev)
+        cp = _dense(kv_cache, "kv_cache", torch.uint8, (num_blocks, 64, 576), dev)
+    return _Attn(qp, cp, H, sm_scale, kt, sp), T, H, dev
+
+
+def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None, out=None, lse=None,
+                   want_lse: bool = True, workspace: Optional[Workspace] = None, stream=None):
+    """Dense attention of the step's new tokens q [T, H, 576] over the paged latent cache
+    (bf16, or FP8 codes with kv_scale): each sees all positions up to its own.  Returns
+    (out [T, H, 512] bf16, lse [T, H] fp32 or None).  Scratch is allocated per call, on the
+    call's stream; the status word is that of `workspace` (status_workspace() by default)."""
+    lib = load_library()
+    at, T, H, dev = _latent_attn(q, kv_cache, sm_scale, kv_scale, batch.num_blocks)
+    cb = _batch_struct(batch, T, dev)
+    status = _ptr((workspace if workspace is not None else status_workspace(q.device)).get(256))
+    with _On(dev, stream) as on:
+        need = lib.dsa_chunk_scratch_size(ctypes.byref(cb), ctypes.byref(at))
+        if need == 0:
+            raise DsaError(2, "dsa_chunk_scratch_size")
+        if out is None:
+            out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        op = _dense(out, "out", torch.bfloat16, (T, H, 512), dev)
+        lp = None if lse is None else _dense(lse, "lse", torch.float32, (T, H), dev)
+        scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
+        rc = lib.dsa_chunk_attn(ctypes.byref(cb), ctypes.byref(at), op, lp, status, scratch.data_ptr(), need, on)
+    if rc != 0:
+        raise DsaError(rc, "dsa_chunk_attn")
+    return out, lse
 
 
 def decode_launch_count(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm_scale: float,

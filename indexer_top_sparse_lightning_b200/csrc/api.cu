@@ -31,17 +31,6 @@ constexpr size_t kStatusBytes = 256;
 constexpr size_t kHeaderBytes = kStatusBytes;
 
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-dsa_status check_batch(const dsa_batch* bt) {
-    if (!bt || bt->batch < 1 || bt->num_tokens < 1 || !bt->seq_lens || !bt->cu_q || !bt->block_table ||
-        bt->max_blocks_per_seq < 1 || bt->num_blocks < 1 || bt->max_seq_len < 1 || bt->max_q_per_seq < 1)
-        return DSA_ERR_INVALID_ARG;
-    if ((int64_t)bt->max_blocks_per_seq * kPage < bt->max_seq_len) return DSA_ERR_INVALID_ARG;
-    if ((int64_t)bt->num_blocks * kPage > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-    return DSA_OK;
-}
-
 dsa_status check_indexer(const dsa_indexer_inputs* ix) {
     if (!ix || !ix->q_idx || !ix->w || !ix->k_cache) return DSA_ERR_INVALID_ARG;
     if (ix->key_dtype != DSA_KEY_BF16 && ix->key_dtype != DSA_KEY_FP8_E4M3 && ix->key_dtype != DSA_KEY_MXFP8)
@@ -60,18 +49,6 @@ dsa_status check_indexer(const dsa_indexer_inputs* ix) {
     if (ix->key_dtype == DSA_KEY_FP8_E4M3 && (reinterpret_cast<uintptr_t>(ix->k_scale) & 3u)) return DSA_ERR_INVALID_ARG;
     return DSA_OK;
 }
-
-dsa_status check_attn(const dsa_attn_inputs* at) {
-    if (!at || !at->q || !at->kv_cache) return DSA_ERR_INVALID_ARG;
-    if (at->H < 1 || at->H > 128) return DSA_ERR_UNSUPPORTED;
-    if (!aligned16(at->q) || !aligned16(at->kv_cache)) return DSA_ERR_INVALID_ARG;
-    if (at->kv_dtype != DSA_KV_BF16 && at->kv_dtype != DSA_KV_FP8) return DSA_ERR_INVALID_ARG;
-    if (at->kv_dtype == DSA_KV_FP8 && (!at->kv_scale || (reinterpret_cast<uintptr_t>(at->kv_scale) & 3u)))
-        return DSA_ERR_INVALID_ARG;
-    if (!(at->sm_scale > 0.0f) || at->sm_scale != at->sm_scale) return DSA_ERR_INVALID_ARG;
-    return DSA_OK;
-}
-
 
 // ------------------------------------------------------------------ indexer planning
 // Fill the fields that depend on the kernel instantiation.

@@ -1,0 +1,143 @@
+// chunk.cu -- host side of dsa_chunk_attn (include/dsa.h): argument checks, the
+// scratch layout, TMA descriptors and the launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "../../include/dsa.h"
+#include "chunk.cuh"
+#include "common.h"
+#include "host.h"
+
+using namespace dsa;
+using namespace dsa::host;
+
+namespace {
+
+// Scratch: [headers][partial slots of the pairs][FP8: the sequences' rows as bf16].
+struct ChunkPlan {
+    int pairs = 0;
+    int64_t pages = 0;          // FP8: pages per sequence of the copy
+    size_t copy_off = 0, total = 0;
+};
+
+dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevInfo& di, ChunkPlan& pl) {
+    if (dsa_status st = check_batch(bt)) return st;
+    if (dsa_status st = check_attn(at)) return st;
+    // (token, head) rows are counted in 32 bits
+    if ((int64_t)bt->num_tokens * at->H > INT32_MAX - ChunkCfg::ROWS) return DSA_ERR_UNSUPPORTED;
+    if (di.sms <= 0) return fail(DSA_ERR_CUDA, "device query failed");
+    if (di.max_smem < ChunkCfg::SMEM) return fail(DSA_ERR_UNSUPPORTED, "device shared memory per block too small");
+    int pmax = di.sms / 2;
+    if (pmax > ChunkCfg::MAX_PAIRS) pmax = ChunkCfg::MAX_PAIRS;
+    // no more pairs than there can be blocks
+    const int64_t rows = (int64_t)bt->num_tokens * at->H;
+    const int64_t tiles = (rows + ChunkCfg::ROWS - 1) / ChunkCfg::ROWS +
+                          (bt->batch < bt->num_tokens ? bt->batch : bt->num_tokens);
+    const int64_t blocks = tiles * ((bt->max_seq_len + ChunkCfg::BLOCK - 1) / ChunkCfg::BLOCK);
+    pl.pairs = (int)(blocks < pmax ? blocks : pmax);
+    pl.copy_off = align256(ChunkCfg::HEAD_BYTES + (size_t)pmax * 4 * (size_t)ChunkCfg::PART_BYTES);
+    pl.total = pl.copy_off;
+    if (at->kv_dtype == DSA_KV_FP8) {
+        pl.pages = ((int64_t)bt->max_seq_len + kPage - 1) / kPage;
+        if (pl.pages * bt->batch > INT32_MAX / kPage) return DSA_ERR_UNSUPPORTED;   // rows of the copy, in 32 bits
+        pl.total += (size_t)pl.pages * bt->batch * kPage * kDqk * 2;
+    }
+    return DSA_OK;
+}
+
+bool rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+    const uint64_t dims[2] = {(uint64_t)kDqk, rows};
+    const uint64_t strides[1] = {(uint64_t)kDqk * 2};
+    const uint32_t box[2] = {64, box_rows};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_chunk_scratch_size(const dsa_batch* batch, const dsa_attn_inputs* at) {
+    ChunkPlan pl;
+    return plan_chunk(batch, at, dev_info(), pl) == DSA_OK ? pl.total : 0;
+}
+
+dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, void* out, float* lse, void* status,
+                          void* scratch, size_t scratch_bytes, void* stream) {
+    ChunkPlan pl;
+    if (dsa_status st = plan_chunk(batch, at, dev_info(), pl)) return st;
+    if (!out || !aligned16(out) || !status || (reinterpret_cast<uintptr_t>(status) & 3u)) return DSA_ERR_INVALID_ARG;
+    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < pl.total) return DSA_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ChunkParams p;
+    memset(&p, 0, sizeof p);
+    p.seq_lens = batch->seq_lens;
+    p.cu_q = batch->cu_q;
+    p.block_table = batch->block_table;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.part = static_cast<uint8_t*>(scratch);
+    p.status = static_cast<uint32_t*>(status);
+    p.B = batch->batch;
+    p.T = batch->num_tokens;
+    p.H = at->H;
+    p.max_blocks = batch->max_blocks_per_seq;
+    p.num_blocks = batch->num_blocks;
+    p.staged = (int32_t)pl.pages;
+    p.scale_log2 = at->sm_scale * 1.4426950408889634f;
+    const void* rows = at->kv_cache;
+    uint64_t nrows = (uint64_t)batch->num_blocks * kPage;
+    if (pl.pages) {
+        PagesParams g;
+        memset(&g, 0, sizeof g);
+        g.seq_lens = batch->seq_lens;
+        g.block_table = batch->block_table;
+        g.codes = static_cast<const uint8_t*>(at->kv_cache);
+        g.scale = at->kv_scale;
+        g.rows = reinterpret_cast<uint16_t*>(p.part + pl.copy_off);
+        g.B = batch->batch;
+        g.max_blocks = batch->max_blocks_per_seq;
+        g.num_blocks = batch->num_blocks;
+        g.pages = (int32_t)pl.pages;
+        kv_fp8_pages_kernel<<<(unsigned)(pl.pages * batch->batch), kPagesThreads, 0, s>>>(g);
+        if (cudaError_t e = cudaGetLastError()) return fail(DSA_ERR_CUDA, "latent copy launch", e);
+        rows = g.rows;
+        nrows = (uint64_t)pl.pages * batch->batch * kPage;
+    }
+    CUtensorMap tm_q, tm_k, tm_v;
+    if (!rows_map(&tm_q, at->q, (uint64_t)batch->num_tokens * at->H, 64) || !rows_map(&tm_k, rows, nrows, 64) ||
+        !rows_map(&tm_v, rows, nrows, 32))
+        return fail(DSA_ERR_CUDA, "tensor map encoding failed");
+    if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(&chunk_attn_kernel), ChunkCfg::SMEM))
+        return fail(DSA_ERR_CUDA, "shared memory attribute", e);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(2 * pl.pairs, 1, 1);
+    cfg.blockDim = dim3(ChunkCfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = ChunkCfg::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, &chunk_attn_kernel, p, tm_q, tm_k, tm_v))
+        return fail(DSA_ERR_CUDA, "attention launch", e);
+    if (pl.pairs < 2) return DSA_OK;
+    cudaLaunchConfig_t ccfg;
+    memset(&ccfg, 0, sizeof ccfg);
+    ccfg.gridDim = dim3(pl.pairs - 1, ChunkCfg::ROWS / (ChunkCfg::COMBINE_THREADS / 32), 1);
+    ccfg.blockDim = dim3(ChunkCfg::COMBINE_THREADS, 1, 1);
+    ccfg.stream = s;
+    ccfg.attrs = attr;
+    ccfg.numAttrs = 1;
+    if (cudaError_t e = cudaLaunchKernelEx(&ccfg, &chunk_combine_kernel, p)) return fail(DSA_ERR_CUDA, "merge launch", e);
+    return DSA_OK;
+}
+
+}  // extern "C"

@@ -39,6 +39,11 @@ constexpr int kMaxDevices = 64;
 // Properties of the current device, queried once per device.
 DevInfo dev_info();
 
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Argument checks shared by the entry points.
+dsa_status check_batch(const dsa_batch* bt);
+dsa_status check_attn(const dsa_attn_inputs* at);
+
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // Mode-0 launches of a plan.
 inline int64_t idx_launches(int64_t windows, int per_launch) { return (windows + per_launch - 1) / per_launch; }

@@ -58,6 +58,7 @@
 // block table and the cache come after the wait.
 #pragma once
 #include "common.h"
+#include "pair.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
@@ -148,30 +149,6 @@ __device__ __forceinline__ int token_sequence(const int32_t* cu_q, int B, int t)
     return lo;
 }
 
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Arrive on an mbarrier of CTA 0 of the pair (a local arrive when this is CTA 0).
-__device__ __forceinline__ void arrive_leader(uint64_t* bar, uint32_t crank) {
-    if (crank == 0) mbar_arrive(bar);
-    else mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
-}
-
-// The contiguous block range of pair `pr` among `np` pairs: [g0, g1) of `total`.
-__device__ __forceinline__ int64_t pair_start(int64_t total, int pr, int np) { return total * pr / np; }
-// The pair whose range holds global block g.
-__device__ __forceinline__ int pair_of_block(int64_t total, int64_t g, int np) {
-    return (int)(((g + 1) * np + total - 1) / total) - 1;
-}
 
 // Resolves block jj of the pair's range: token, first/last block of its segment.
 struct SfaBlock {
