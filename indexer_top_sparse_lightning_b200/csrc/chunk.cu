@@ -47,11 +47,13 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
     return DSA_OK;
 }
 
-bool rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
-    const uint64_t dims[2] = {(uint64_t)kDqk, rows};
-    const uint64_t strides[1] = {(uint64_t)kDqk * 2};
-    const uint32_t box[2] = {64, box_rows};
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+// Rows of 576 as [64 columns, rows, 9 chunks]: a box's 64-column chunks come out one
+// after another, each in the 128-byte rows that the MMA operands have.
+bool rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_chunks) {
+    const uint64_t dims[3] = {64, rows, (uint64_t)ChunkCfg::KCH};
+    const uint64_t strides[2] = {(uint64_t)kDqk * 2, 128};
+    const uint32_t box[3] = {64, box_rows, box_chunks};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -106,8 +108,8 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
         nrows = (uint64_t)pl.pages * batch->batch * kPage;
     }
     CUtensorMap tm_q, tm_k, tm_v;
-    if (!rows_map(&tm_q, at->q, (uint64_t)batch->num_tokens * at->H, 64) || !rows_map(&tm_k, rows, nrows, 64) ||
-        !rows_map(&tm_v, rows, nrows, 32))
+    if (!rows_map(&tm_q, at->q, (uint64_t)batch->num_tokens * at->H, 64, ChunkCfg::KCH) ||
+        !rows_map(&tm_k, rows, nrows, 64, 3) || !rows_map(&tm_v, rows, nrows, 32, 2))
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");
     if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(&chunk_attn_kernel), ChunkCfg::SMEM))
         return fail(DSA_ERR_CUDA, "shared memory attribute", e);

@@ -22,14 +22,16 @@
 //       2k + c), nine K-chunks of 64 columns;
 //   O += P.V: M = 128 rows, N = 256 value columns twice (CTA c holds columns
 //       128c.. and 256 + 128c.. of both pages), K = 128 positions.
-// Both operands come through ONE ring of 8 KB slots filled by one thread in
-// the very order in which the MMAs consume them (a 64 x 64 box of keys, or 32
-// rows x 128 value columns), across block and tile boundaries: 15 slots keep
-// 120 KB per SM in flight, more than a block's worth, with no fixed split
-// between keys and values.  S of block k + 1 is computed before P.V of block k,
-// so the softmax of one block runs under the products of its neighbours.
-// Loads of both CTAs are counted on CTA 0's barriers (the two-CTA form of the
-// tiled load), so nobody forwards arrivals.
+// Keys and values have a ring each (a whole block of keys in three groups of
+// 64 rows x 192 columns, a whole block of values in four groups of 32 rows x 256
+// columns of the pair's 512), a loading warp each and an issuing warp each: one
+// warp cannot issue a block's 52 MMAs and wait for their operands in the time
+// that the MMAs take.  The issuing warps run ahead of one another as far as the
+// two score buffers and the one weight buffer allow, across tiles too, so the
+// softmax of one block runs under the products of its neighbours.  Every group is
+// one or two copies (the tensor maps have the 64-column chunks of a row as their
+// outermost dimension), counted for both CTAs on CTA 0's barriers (the two-CTA
+// form of the tiled load), which CTA 0's loaders arm for both.
 //
 // What bounds it.  2176 * 128 * 128 operations per block of the pair take about
 // 1.15 us at the tensor core's rate, and the block's operands are 278 KB through
@@ -45,13 +47,14 @@
 // tokens that see one have a non-finite score already).  Only the slots at the
 // tile's causal edge take this path (the "fixer" warp).
 //
-// Roles per CTA (256 threads):
+// Roles per CTA (320 threads):
 //   warps 0-3   softmax and epilogue (thread L <-> TMEM lane L: row 64c + L%64,
 //               positions 64*(L/64).. of a block)
-//   warp 4      TMEM allocation; CTA 0: MMA issuer
-//   warp 5      loads of keys and values
-//   warp 6      segments (runs of one tile's blocks) and the loads of Q
-//   warp 7      fixer
+//   warp 4      TMEM allocation; CTA 0: issues the score MMAs
+//   warp 5      CTA 0: issues the value MMAs
+//   warps 6, 7  loads of keys, of values
+//   warp 8      segments (runs of one tile's blocks) and the loads of Q
+//   warp 9      fixer
 #pragma once
 #include "common.h"
 #include "fp8row.cuh"
@@ -64,19 +67,22 @@ struct ChunkCfg {
     static constexpr int ROWS = 128;                    // (token, head) rows of a tile
     static constexpr int BLOCK = 128;                   // positions of a block (two pages)
     static constexpr int KCH = 9;                       // 64-column chunks of a latent row
-    static constexpr int SLOT = 8192;
-    static constexpr int NSLOT = 15;
+    static constexpr int KGROUPS = 3;                   // groups of a block's keys: 64 rows x 3 chunks
+    static constexpr int KGROUP = 3 * 8192;
+    static constexpr int VGROUPS = 4;                   // groups of a block's values: 32 rows x 4 chunks (this CTA's)
+    static constexpr int VGROUP = 4 * 4096;
     static constexpr int Q_BYTES = KCH * 64 * 128;      // this CTA's 64 rows
     static constexpr int P_BYTES = 64 * BLOCK * 2;      // [64 rows x 128 positions] bf16: two 64-position chunks
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
-    static constexpr int OFF_RING = OFF_P + 2 * P_BYTES;
-    static constexpr int OFF_XM = OFF_RING + NSLOT * SLOT;   // partner exchange, two buffers of 128 floats
+    static constexpr int OFF_K = OFF_P + P_BYTES;
+    static constexpr int OFF_V = OFF_K + KGROUPS * KGROUP;
+    static constexpr int OFF_XM = OFF_V + VGROUPS * VGROUP;   // partner exchange, two buffers of 128 floats
     static constexpr int OFF_MISC = OFF_XM + 2 * 128 * 4;
     static constexpr int MISC_BYTES = 1024;
     static constexpr int SMEM = 1024 + OFF_MISC + MISC_BYTES;
-    static constexpr int THREADS = 256;
-    static constexpr int MMA_WARP = 4, LOAD_WARP = 5, SEG_WARP = 6, FIX_WARP = 7;
+    static constexpr int THREADS = 320;
+    static constexpr int QK_WARP = 4, PV_WARP = 5, KEY_WARP = 6, VALUE_WARP = 7, SEG_WARP = 8, FIX_WARP = 9;
     static constexpr int NSEG = 4;                      // segment ring
     static constexpr int TMEM_COLS = 512;               // O: [0, 256), two score buffers of 64 from column 256
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, BLOCK, false, false);
@@ -90,7 +96,7 @@ struct ChunkCfg {
     static constexpr int COMBINE_THREADS = 256;
 };
 static_assert(ChunkCfg::SMEM <= 232448, "shared memory exceeds the per-CTA limit");
-static_assert(ChunkCfg::OFF_P % 1024 == 0 && ChunkCfg::OFF_RING % 1024 == 0, "swizzled operands need 1024-byte alignment");
+static_assert(ChunkCfg::OFF_P % 1024 == 0 && ChunkCfg::OFF_K % 1024 == 0 && ChunkCfg::OFF_V % 1024 == 0, "swizzled operands need 1024-byte alignment");
 static_assert(ChunkCfg::MAX_PAIRS * 16 <= ChunkCfg::HEAD_BYTES, "one header per pair");
 
 struct ChunkParams {
@@ -120,13 +126,15 @@ struct ChunkSeg {
 };
 
 struct ChunkMisc {
-    uint64_t full[ChunkCfg::NSLOT];     // (CTA 0) a slot of both CTAs is ready for the MMAs
-    uint64_t empty[ChunkCfg::NSLOT];    // its MMAs have completed
-    uint64_t land[ChunkCfg::NSLOT];     // bytes of a slot that the fixer looks at have landed
-    uint64_t q_full;                    // (CTA 0) Q of both CTAs
+    uint64_t k_full[ChunkCfg::KGROUPS];   // (CTA 0) the key group is ready in both CTAs
+    uint64_t k_empty[ChunkCfg::KGROUPS];  // its MMAs have completed
+    uint64_t v_full[ChunkCfg::VGROUPS];   // (CTA 0) the value group is ready in both CTAs
+    uint64_t v_empty[ChunkCfg::VGROUPS];
+    uint64_t v_land[ChunkCfg::VGROUPS];   // the group has landed, for the fixer to look at
+    uint64_t q_full;                      // (CTA 0) Q of both CTAs
     uint64_t q_empty;
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-    uint64_t o_full, o_empty, drain;
+    uint64_t s_full[2], s_empty[2], p_full, p_empty;
+    uint64_t o_full, o_empty, drain[2];
     uint64_t seg_full[ChunkCfg::NSEG], seg_empty[ChunkCfg::NSEG];
     ChunkSeg seg[ChunkCfg::NSEG];
     uint64_t wait_ns;
@@ -209,7 +217,25 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
     return total;
 }
 
-// The rows at or past this row limit of a block see nothing of it.
+// Waits of a whole warp: one lane polls (32 lanes' polls would each take a turn in
+// the shared-memory pipe that every other barrier operation needs), the rest
+// sleep at the warp's barrier.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_spin(bar, parity, abort, limit_ns);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// The same in warps that act through an elected lane; the answer is uniform.
+__device__ __forceinline__ bool elected_wait(bool el, uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             uint64_t limit_ns) {
+    bool ok = true;
+    if (el) ok = mbar_spin(bar, parity, abort, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The 32-position groups of a block that the value product runs over.
 struct ChunkBlock {
     int ngroups;              // 32-position groups that some row sees (1..4)
     int fix_from;             // first group that the fixer looks at (ngroups: none)
@@ -232,7 +258,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     uint8_t* smem = align_shared(smem_raw, 1024);
     uint8_t* s_q = smem + Cfg::OFF_Q;
     uint8_t* s_p = smem + Cfg::OFF_P;
-    uint8_t* s_ring = smem + Cfg::OFF_RING;
+    uint8_t* s_k = smem + Cfg::OFF_K;
+    uint8_t* s_v = smem + Cfg::OFF_V;
     float* s_xm = reinterpret_cast<float*>(smem + Cfg::OFF_XM);
     ChunkMisc* m = reinterpret_cast<ChunkMisc*>(smem + Cfg::OFF_MISC);
     volatile int* abort = &m->abort;
@@ -243,31 +270,35 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     const int pair = (int)(blockIdx.x >> 1);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Cfg::NSLOT; ++i) {
-            mbar_init(&m->full[i], 2);      // one arrival per CTA, with that CTA's bytes
-            mbar_init(&m->empty[i], 1);
-            mbar_init(&m->land[i], 1);
+        for (int i = 0; i < Cfg::KGROUPS; ++i) {
+            mbar_init(&m->k_full[i], 1);    // CTA 0's loader, for both CTAs
+            mbar_init(&m->k_empty[i], 1);
+        }
+        for (int i = 0; i < Cfg::VGROUPS; ++i) {
+            mbar_init(&m->v_full[i], 2);    // two by CTA 0's loader, or one by each CTA's fixer
+            mbar_init(&m->v_empty[i], 1);
+            mbar_init(&m->v_land[i], 1);
         }
         mbar_init(&m->q_full, 2);
         mbar_init(&m->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->s_full[i], 1);
             mbar_init(&m->s_empty[i], 8);   // one arrival per softmax warp of both CTAs
-            mbar_init(&m->p_full[i], 8);
-            mbar_init(&m->p_empty[i], 1);
+            mbar_init(&m->drain[i], 1);
         }
+        mbar_init(&m->p_full, 8);
+        mbar_init(&m->p_empty, 1);
         mbar_init(&m->o_full, 1);
         mbar_init(&m->o_empty, 8);
-        mbar_init(&m->drain, 1);
         for (int i = 0; i < Cfg::NSEG; ++i) {
             mbar_init(&m->seg_full[i], 1);
-            mbar_init(&m->seg_empty[i], crank == 0 ? 7 : 6);   // softmax, load and fixer warps; CTA 0: the issuer too
+            mbar_init(&m->seg_empty[i], crank == 0 ? 9 : 7);   // softmax, loading and fixer warps; CTA 0: the issuers too
         }
         m->abort = 0;
         m->start_b = -1;
         fence_mbar_init();
     }
-    if (warp == Cfg::MMA_WARP) {
+    if (warp == Cfg::QK_WARP) {
         tmem_alloc_2cta(&m->tmem_base, Cfg::TMEM_COLS);
         tmem_relinquish_2cta();
     }
@@ -358,7 +389,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             const uint32_t q_full = mapa_shared(smem_u32(&m->q_full), 0);
             while (true) {
                 const int r = ns % Cfg::NSEG;
-                if (!mbar_wait(&m->seg_empty[r], ((ns / Cfg::NSEG) & 1) ^ 1, abort, wlim)) {
+                if (!mbar_spin(&m->seg_empty[r], ((ns / Cfg::NSEG) & 1) ^ 1, abort, wlim)) {
                     ok = false;
                     break;
                 }
@@ -392,13 +423,12 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 if (sg.part == 1)
                     head = make_int4(sg.row0, sg.nrows, pair_of_block(total, tile_g0 + nb - 1, np) - pair + 1, 0);
                 // Q, once every QK of the segment before has completed
-                if (ns > 0 && !mbar_wait(&m->q_empty, (ns - 1) & 1, abort, wlim)) {
+                if (ns > 0 && !mbar_spin(&m->q_empty, (ns - 1) & 1, abort, wlim)) {
                     ok = false;
                     break;
                 }
                 mbar_arrive_expect_tx_cluster(q_full, Cfg::Q_BYTES);
-                for (int kb = 0; kb < Cfg::KCH; ++kb)
-                    tma_load_2d_pair(s_q + kb * 8192, &tm_q, q_full, kb * 64, sg.row0 + 64 * (int)crank);
+                tma_load_3d_pair(s_q, &tm_q, q_full, 0, sg.row0 + 64 * (int)crank, 0);
                 ++ns;
                 g = stop;
                 if (g < g1) {
@@ -415,236 +445,244 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             if (crank == 0) reinterpret_cast<int4*>(p.part)[pair] = head;
         }
         __syncwarp();
-    } else if (warp == Cfg::LOAD_WARP) {
-        // ---------------------------------------------------------------- loads of keys and values
+    } else if (warp == Cfg::KEY_WARP || warp == Cfg::VALUE_WARP) {
+        // ---------------------------------------------------------------- loads of keys, of values
+        // The whole warp runs the schedule and one elected lane acts, so that addresses and
+        // coordinates stay in uniform registers (per-lane values would have to be moved there for
+        // every copy).  CTA 0 announces the bytes of both CTAs (both see the same page ids), so
+        // that CTA 1 only issues its copies.
+        const bool keys = warp == Cfg::KEY_WARP;
+        const bool el = elect_one();
         // test hook: the second CTA never loads
         bool ok = !(crank == 1 && (m->inject & 4u));
-        uint32_t n = 0;                    // slots so far
+        bool bad = false;
+        uint32_t n = 0;                    // blocks (keys) or groups (values) so far
+        const uint32_t k_lead = mapa_shared(smem_u32(&m->k_full[0]), 0), v_lead = mapa_shared(smem_u32(&m->v_full[0]), 0);
         ChunkSeg sg = {};
-        int pbase = 0, pid = -1;           // the lane's page id: page pbase + lane of the sequence
-        auto refill = [&](int k) {
-            pbase = 2 * k;
-            const int page = pbase + lane;
-            pid = -1;
-            if (page < p.max_blocks && page * kPage < sg.see) {
-                const int id = __ldg(p.block_table + (int64_t)sg.b * p.max_blocks + page);
-                if (id >= 0 && id < p.num_blocks) pid = p.staged ? sg.b * p.staged + page : id;
-                else atomicCAS(p.status, 0u, (uint32_t)kStBounds);
-            }
+        const int32_t* table = nullptr;
+        auto page_id = [&](int page) -> int {          // -1: nobody sees the page; -2: a bad id
+            if (page >= p.max_blocks || page * kPage >= sg.see) return -1;
+            const int id = __ldg(table + page);
+            return id >= 0 && id < p.num_blocks ? (p.staged ? sg.b * p.staged + page : id) : -2;
         };
-        auto slot_free = [&]() -> bool {
-            const int r = n % Cfg::NSLOT;
-            return __all_sync(0xffffffffu, mbar_wait(&m->empty[r], ((n / Cfg::NSLOT) & 1) ^ 1, abort, wlim));
-        };
-        auto load_keys = [&](int k) -> bool {
-            const int id = __shfl_sync(0xffffffffu, pid, 2 * k + (int)crank - pbase);
-            for (int kb = 0; kb < Cfg::KCH; ++kb) {
-                if (!slot_free()) return false;
-                const int r = n % Cfg::NSLOT;
-                if (lane == 0) {
-                    const uint32_t bar = mapa_shared(smem_u32(&m->full[r]), 0);
-                    // a page that nobody sees is not loaded: its scores are replaced whatever they are
-                    if (id >= 0) {
-                        mbar_arrive_expect_tx_cluster(bar, Cfg::SLOT);
-                        tma_load_2d_pair(s_ring + r * Cfg::SLOT, &tm_k, bar, kb * 64, id * kPage);
-                    } else {
-                        mbar_arrive_remote(bar);
-                    }
-                }
-                __syncwarp();
-                ++n;
+        auto load_keys = [&](int id0, int id1) -> bool {
+            const int id = crank == 0 ? id0 : id1;
+            // a page that nobody sees is not loaded: its scores are replaced whatever they are
+            const uint32_t bytes = (uint32_t)Cfg::KGROUP * ((id0 >= 0) + (id1 >= 0));
+            const bool mine = el && id >= 0;
+#pragma unroll 1
+            for (int g = 0; g < Cfg::KGROUPS; ++g) {
+                if (!elected_wait(el, &m->k_empty[g], (n & 1) ^ 1, abort, wlim)) return false;
+                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[g], bytes);
+                if (mine) tma_load_3d_pair(s_k + g * Cfg::KGROUP, &tm_k, k_lead + 8 * g, 0, id * kPage, 3 * g);
             }
+            ++n;
             return true;
         };
-        auto load_values = [&](int k) -> bool {
-            const ChunkBlock cb = chunk_block(sg, k);
-            for (int g = 0; g < cb.ngroups; ++g) {
-                const int id = __shfl_sync(0xffffffffu, pid, 2 * k + (g >> 1) - pbase);
-                for (int h = 0; h < 2; ++h) {
-                    if (!slot_free()) return false;
-                    const int r = n % Cfg::NSLOT;
-                    uint8_t* dst = s_ring + r * Cfg::SLOT;
-                    const bool fix = g >= cb.fix_from;
-                    if (id < 0) {          // a bad page id (reported): zeros
-                        for (int i = lane; i < Cfg::SLOT / 16; i += 32)
-                            reinterpret_cast<uint4*>(dst)[i] = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        const uint32_t bar = mapa_shared(smem_u32(fix ? &m->land[r] : &m->full[r]), fix ? crank : 0);
-                        if (id >= 0) {
-                            const int x = 256 * h + 128 * (int)crank, y = id * kPage + 32 * (g & 1);
-                            mbar_arrive_expect_tx_cluster(bar, Cfg::SLOT);
-                            tma_load_2d_pair(dst, &tm_v, bar, x, y);
-                            tma_load_2d_pair(dst + Cfg::SLOT / 2, &tm_v, bar, x + 64, y);
-                        } else {
-                            mbar_arrive_remote(bar);
-                        }
-                    }
+        auto load_values = [&](const ChunkBlock& cb, int id0, int id1) -> bool {
+#pragma unroll 1
+            for (int g = 0; g < cb.ngroups; ++g, ++n) {
+                const uint32_t r = n % Cfg::VGROUPS;
+                if (!elected_wait(el, &m->v_empty[r], ((n / Cfg::VGROUPS) & 1) ^ 1, abort, wlim)) return false;
+                const int id = g < 2 ? id0 : id1;
+                const bool fix = g >= cb.fix_from;
+                uint8_t* dst = s_v + r * Cfg::VGROUP;
+                if (id < 0) {              // a bad page id: zeros
+                    for (int i = lane; i < Cfg::VGROUP / 16; i += 32)
+                        reinterpret_cast<uint4*>(dst)[i] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
                     __syncwarp();
-                    ++n;
+                }
+                const int y = id * kPage + 32 * (g & 1), z = 2 * (int)crank;
+                if (!el) continue;
+                if (fix) {
+                    // this CTA's fixer looks at the rows before the MMAs may
+                    if (id >= 0) {
+                        mbar_arrive_expect_tx(&m->v_land[r], Cfg::VGROUP);
+                        tma_load_3d(dst, &tm_v, &m->v_land[r], 0, y, z);
+                        tma_load_3d(dst + Cfg::VGROUP / 2, &tm_v, &m->v_land[r], 0, y, z + 4);
+                    } else {
+                        mbar_arrive(&m->v_land[r]);
+                    }
+                } else if (id >= 0) {
+                    if (crank == 0) {
+                        mbar_arrive_expect_tx(&m->v_full[r], 2 * Cfg::VGROUP);
+                        mbar_arrive(&m->v_full[r]);
+                    }
+                    tma_load_3d_pair(dst, &tm_v, v_lead + 8 * r, 0, y, z);
+                    tma_load_3d_pair(dst + Cfg::VGROUP / 2, &tm_v, v_lead + 8 * r, 0, y, z + 4);
+                } else {
+                    arrive_leader(&m->v_full[r], crank);
                 }
             }
             return true;
         };
         for (int ns = 0; ok; ++ns) {
-            const int r = ns % Cfg::NSEG;
-            if (!__all_sync(0xffffffffu, mbar_wait(&m->seg_full[r], (ns / Cfg::NSEG) & 1, abort, wlim))) {
+            const int sr = ns % Cfg::NSEG;
+            if (!elected_wait(el, &m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim)) {
                 ok = false;
                 break;
             }
-            sg = m->seg[r];
+            sg = m->seg[sr];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&m->seg_empty[r]);
+            if (el) mbar_arrive(&m->seg_empty[sr]);
             if (sg.b < 0) break;
-            refill(sg.k0);
-            ok = load_keys(sg.k0);
-            for (int k = sg.k0; ok && k < sg.k1; ++k) {
-                if (2 * (k + 1) + 1 >= pbase + 32) refill(k);
-                if (k + 1 < sg.k1) ok = load_keys(k + 1);
-                if (ok) ok = load_values(k);
+            table = p.block_table + (int64_t)sg.b * p.max_blocks;
+            const int k0 = __shfl_sync(0xffffffffu, sg.k0, 0), k1 = __shfl_sync(0xffffffffu, sg.k1, 0);
+            // page ids one block ahead, so that no load waits for one
+            int a0 = page_id(2 * k0), a1 = page_id(2 * k0 + 1);
+            for (int k = k0; ok && k < k1; ++k) {
+                const int b0 = page_id(2 * k + 2), b1 = page_id(2 * k + 3);
+                if (keys) {
+                    bad = bad || a0 == -2 || a1 == -2;
+                    ok = load_keys(a0, a1);
+                } else {
+                    ok = load_values(chunk_block(sg, k), a0, a1);
+                }
+                a0 = b0;
+                a1 = b1;
             }
         }
+        if (bad && el) atomicCAS(p.status, 0u, (uint32_t)kStBounds);
         if (!ok) *abort = 1;
     } else if (warp == Cfg::FIX_WARP) {
         // ---------------------------------------------------------------- value rows at the causal edge
         bool ok = true;
-        uint32_t n = 0, phase = 0;         // slots so far; next phase of each land barrier
+        uint32_t n = 0, phase = 0;         // groups so far; next phase of each land barrier
         for (int ns = 0; ok; ++ns) {
-            const int r = ns % Cfg::NSEG;
-            if (!__all_sync(0xffffffffu, mbar_wait(&m->seg_full[r], (ns / Cfg::NSEG) & 1, abort, wlim))) {
+            const int sr = ns % Cfg::NSEG;
+            if (!warp_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim)) {
                 ok = false;
                 break;
             }
-            const ChunkSeg sg = m->seg[r];
+            const ChunkSeg sg = m->seg[sr];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&m->seg_empty[r]);
+            if (lane == 0) mbar_arrive(&m->seg_empty[sr]);
             if (sg.b < 0) break;
-            n += Cfg::KCH;                 // keys of the first block
             for (int k = sg.k0; ok && k < sg.k1; ++k) {
-                if (k + 1 < sg.k1) n += Cfg::KCH;
                 const ChunkBlock cb = chunk_block(sg, k);
-                n += 2 * cb.fix_from;
-                for (int g = cb.fix_from; ok && g < cb.ngroups; ++g)
-                    for (int h = 0; ok && h < 2; ++h, ++n) {
-                        const int sl = n % Cfg::NSLOT;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&m->land[sl], (phase >> sl) & 1, abort, wlim));
-                        if (!ok) break;
-                        phase ^= 1u << sl;
-                        // lane = row of the group; its sixteen 16-byte pieces, in an order that
-                        // spreads the lanes over the banks
-                        uint8_t* row = s_ring + sl * Cfg::SLOT + lane * 128;
-                        const int pos = k * Cfg::BLOCK + 32 * g + lane;
-                        bool zero = pos >= sg.see;
-                        if (!zero && pos >= sg.see_all) {
-                            uint32_t bad = 0;
+                n += cb.fix_from;
+                for (int g = cb.fix_from; ok && g < cb.ngroups; ++g, ++n) {
+                    const uint32_t r = n % Cfg::VGROUPS;
+                    ok = warp_wait(&m->v_land[r], (phase >> r) & 1, abort, wlim);
+                    if (!ok) break;
+                    phase ^= 1u << r;
+                    // lane = row of the group: four 64-column chunks of 128 bytes, 4096 apart, their
+                    // 16-byte parts in an order that spreads the lanes over the banks
+                    uint8_t* row = s_v + r * Cfg::VGROUP + lane * 128;
+                    auto part = [&](int q) -> uint4* {
+                        return reinterpret_cast<uint4*>(row + (q >> 3) * 4096 + (((q + lane) & 7) << 4));
+                    };
+                    const int pos = k * Cfg::BLOCK + 32 * g + lane;
+                    bool zero = pos >= sg.see;
+                    if (!zero && pos >= sg.see_all) {
+                        uint32_t odd = 0;  // an exponent of all ones
+#pragma unroll 1
+                        for (int q = 0; q < 32; ++q) {
+                            const uint4 v = *part(q);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                            for (int q = 0; q < 16; ++q) {
-                                const uint4 v = *reinterpret_cast<const uint4*>(
-                                    row + (q >> 3) * (Cfg::SLOT / 2) + (((q + lane) & 7) << 4));
-                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    bad |= (uint32_t)((w[e] & 0x7F80u) == 0x7F80u) | (uint32_t)((w[e] & 0x7F800000u) == 0x7F800000u);
-                            }
-                            zero = bad != 0;
+                            for (int e = 0; e < 4; ++e)
+                                odd |= (uint32_t)((w[e] & 0x7F80u) == 0x7F80u) | (uint32_t)((w[e] & 0x7F800000u) == 0x7F800000u);
                         }
-                        if (zero)
-#pragma unroll
-                            for (int q = 0; q < 16; ++q)
-                                *reinterpret_cast<uint4*>(row + (q >> 3) * (Cfg::SLOT / 2) + (((q + lane) & 7) << 4)) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) arrive_leader(&m->full[sl], crank);
+                        zero = odd != 0;
                     }
+                    if (zero)
+#pragma unroll 1
+                        for (int q = 0; q < 32; ++q) *part(q) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader(&m->v_full[r], crank);
+                }
             }
         }
         if (!ok) *abort = 1;
-    } else if (warp == Cfg::MMA_WARP) {
+    } else if (warp == Cfg::QK_WARP || warp == Cfg::PV_WARP) {
+        // ---------------------------------------------------------------- MMA issuers (CTA 0)
+        // The whole warp runs the schedule and one elected lane issues, so that the operand
+        // descriptors stay in uniform registers: 30 cycles per MMA where descriptors kept per
+        // lane cost 51 (the MMAs themselves take 32 and 64).  Descriptors differ from a base by
+        // multiples of 16 bytes in their low words.
+        const bool qk = warp == Cfg::QK_WARP;
         if (crank == 0) {
-            // ------------------------------------------------------------ MMA issuer
+            const bool el = elect_one();
             bool ok = true;
-            if (lane == 0) {
-                const uint32_t q_addr = smem_u32(s_q), p_addr = smem_u32(s_p), r_addr = smem_u32(s_ring);
-                uint32_t n = 0, blk = 0;   // slots and blocks so far
-                auto slot = [&](uint32_t& addr) -> bool {
-                    const int r = n % Cfg::NSLOT;
-                    addr = r_addr + r * Cfg::SLOT;
-                    if (!mbar_wait(&m->full[r], (n / Cfg::NSLOT) & 1, abort, wlim)) return false;
-                    tc_fence_after();
-                    return true;
-                };
-                auto issue_qk = [&](uint32_t bi, bool last) -> bool {
-                    const int b = bi & 1;
-                    if (!mbar_wait(&m->s_empty[b], ((bi >> 1) & 1) ^ 1, abort, wlim)) return false;
-                    tc_fence_after();
-                    for (int kb = 0; kb < Cfg::KCH; ++kb) {
-                        uint32_t a;
-                        if (!slot(a)) return false;
+            const uint64_t q_desc = sdesc_sw128(smem_u32(s_q), 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(s_k), 16, 1024);
+            const uint64_t p_desc = sdesc_sw128(smem_u32(s_p), 16, 1024);
+            // V [16 positions x 128 columns per CTA] MN-major: 64-column chunks of 32 rows 4096 B
+            // apart (LBO), 8-row groups 1024 B (SBO)
+            const uint64_t v_desc = sdesc_sw128(smem_u32(s_v), 4096, 1024);
+            uint32_t blk = 0, n = 0;       // blocks and value groups so far
+            auto issue_qk = [&](bool last) -> bool {
+                // scores of this buffer's block before have been read
+                if (!elected_wait(el, &m->s_empty[blk & 1], ((blk >> 1) & 1) ^ 1, abort, wlim)) return false;
+                tc_fence_after();
+                const uint32_t d = tm_s + (blk & 1) * 64;
+#pragma unroll 1
+                for (int g = 0; g < Cfg::KGROUPS; ++g) {
+                    if (!elected_wait(el, &m->k_full[g], blk & 1, abort, wlim)) return false;
+#pragma unroll 1
+                    for (int kb = 3 * g; kb < 3 * g + 3; ++kb)
 #pragma unroll
                         for (int k16 = 0; k16 < 4; ++k16)
-                            umma_bf16_2cta(tm_s + b * 64, sdesc_sw128(q_addr + kb * 8192 + k16 * 32, 16, 1024),
-                                           sdesc_sw128(a + k16 * 32, 16, 1024), Cfg::IDESC_QK, (kb | k16) != 0);
-                        umma_commit_2cta(&m->empty[n % Cfg::NSLOT], 3);
-                        ++n;
-                    }
-                    umma_commit_2cta(&m->s_full[b], 3);
-                    if (last) umma_commit_2cta(&m->q_empty, 3);
-                    return true;
-                };
-                auto issue_pv = [&](uint32_t bi, const ChunkBlock& cb, bool first, bool last, int ns) -> bool {
-                    const int b = bi & 1;
-                    if (!mbar_wait(&m->p_full[b], (bi >> 1) & 1, abort, wlim)) return false;
-                    // O of the segment before must have been read by both epilogues
-                    if (first && ns > 0 && !mbar_wait(&m->o_empty, (ns - 1) & 1, abort, wlim)) return false;
-                    tc_fence_after();
-                    for (int g = 0; g < cb.ngroups; ++g)
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t a;
-                            if (!slot(a)) return false;
-#pragma unroll
-                            for (int s16 = 0; s16 < 2; ++s16)
-                                // A = P [64 rows x 16 positions] K-major; B = V [16 positions x 128
-                                // columns per CTA] MN-major: 64-column chunks half a slot apart (LBO),
-                                // 8-row groups 1024 B (SBO)
-                                umma_bf16_2cta(tm_o + h * 128,
-                                               sdesc_sw128(p_addr + b * Cfg::P_BYTES + (g >> 1) * 8192 +
-                                                               ((g & 1) * 2 + s16) * 32, 16, 1024),
-                                               sdesc_sw128(a + s16 * 16 * 128, Cfg::SLOT / 2, 1024), Cfg::IDESC_PV,
-                                               !first || g > 0 || s16 > 0);
-                            umma_commit_2cta(&m->empty[n % Cfg::NSLOT], 3);
-                            ++n;
-                        }
-                    umma_commit_2cta(&m->p_empty[b], 3);
-                    if (last) umma_commit_2cta(&m->o_full, 3);
-                    return true;
-                };
-                for (int ns = 0; ok; ++ns) {
-                    const int r = ns % Cfg::NSEG;
-                    if (!mbar_wait(&m->seg_full[r], (ns / Cfg::NSEG) & 1, abort, wlim)) {
-                        ok = false;
-                        break;
-                    }
-                    const ChunkSeg sg = m->seg[r];
-                    mbar_arrive(&m->seg_empty[r]);
-                    if (sg.b < 0) break;
-                    ok = mbar_wait(&m->q_full, ns & 1, abort, wlim);
-                    if (!ok) break;
-                    tc_fence_after();
-                    ok = issue_qk(blk, sg.k0 + 1 == sg.k1);
-                    for (int k = sg.k0; ok && k < sg.k1; ++k, ++blk) {
-                        if (k + 1 < sg.k1) ok = issue_qk(blk + 1, k + 2 == sg.k1);
-                        if (ok) ok = issue_pv(blk, chunk_block(sg, k), k == sg.k0, k + 1 == sg.k1, ns);
-                    }
+                            if (el)
+                                umma_bf16_2cta(d, q_desc + (kb * 512 + k16 * 2), k_desc + (kb * 512 + k16 * 2), Cfg::IDESC_QK,
+                                               (kb | k16) != 0);
+                    if (el) umma_commit_2cta(&m->k_empty[g], 3);
                 }
-                volatile int no_abort = 0;
-                umma_commit_2cta(&m->drain, 1);
-                mbar_wait(&m->drain, 0, &no_abort, wlim);
-                if (!ok) *abort = 1;
+                if (el) umma_commit_2cta(&m->s_full[blk & 1], 3);
+                if (last && el) umma_commit_2cta(&m->q_empty, 3);
+                return true;
+            };
+            auto issue_pv = [&](int ngroups, bool first, bool last) -> bool {
+                if (!elected_wait(el, &m->p_full, blk & 1, abort, wlim)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int g = 0; g < ngroups; ++g) {
+                    const uint32_t r = n % Cfg::VGROUPS;
+                    if (!elected_wait(el, &m->v_full[r], (n / Cfg::VGROUPS) & 1, abort, wlim)) return false;
+                    const uint64_t vd = v_desc + r * (Cfg::VGROUP / 16);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int s16 = 0; s16 < 2; ++s16)
+                            if (el)        // A = P [64 rows x 16 positions] K-major
+                                umma_bf16_2cta(tm_o + h * 128, p_desc + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
+                                               vd + (h * 512 + s16 * 128), Cfg::IDESC_PV, g > 0 || s16 > 0 || !first);
+                    if (el) umma_commit_2cta(&m->v_empty[r], 3);
+                    ++n;
+                }
+                if (el) umma_commit_2cta(&m->p_empty, 3);
+                if (last && el) umma_commit_2cta(&m->o_full, 3);
+                return true;
+            };
+            for (int ns = 0; ok; ++ns) {
+                const int sr = ns % Cfg::NSEG;
+                if (!elected_wait(el, &m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim)) {
+                    ok = false;
+                    break;
+                }
+                const ChunkSeg sg = m->seg[sr];
+                __syncwarp();
+                if (el) mbar_arrive(&m->seg_empty[sr]);
+                if (sg.b < 0) break;
+                const int nb = __shfl_sync(0xffffffffu, sg.k1 - sg.k0, 0);
+                // only the segment's last block can have positions that no row sees
+                const int end_groups = __shfl_sync(0xffffffffu, chunk_block(sg, sg.k1 - 1).ngroups, 0);
+                if (qk) ok = elected_wait(el, &m->q_full, ns & 1, abort, wlim);
+                // O of the segment before must have been read by both epilogues
+                else if (ns > 0) ok = elected_wait(el, &m->o_empty, (ns - 1) & 1, abort, wlim);
+                for (int i = 0; ok && i < nb; ++i, ++blk)
+                    ok = qk ? issue_qk(i + 1 == nb) : issue_pv(i + 1 == nb ? end_groups : Cfg::VGROUPS, i == 0, i + 1 == nb);
+            }
+            volatile int no_abort = 0;
+            if (el) {
+                umma_commit_2cta(&m->drain[qk ? 0 : 1], 1);
+                mbar_spin(&m->drain[qk ? 0 : 1], 0, &no_abort, wlim);
             }
             __syncwarp();
+            if (!ok) *abort = 1;
         }
     } else {
         // ---------------------------------------------------------------- softmax + epilogue
@@ -660,7 +698,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         // by named barriers), so the named barriers always match.
         for (int ns = 0;; ++ns) {
             const int sr = ns % Cfg::NSEG;
-            const bool there = mbar_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim);
+            const bool there = warp_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim);
             ok = named_bar_and(1, 128, ok && there);
             if (!ok) break;
             const ChunkSeg sg = m->seg[sr];
@@ -686,7 +724,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 const uint32_t u = (blk >> 1) & 1;
                 const bool this_ok = next_ok;
                 if (k + 1 < sg.k1) next_ok = page_ok(k + 1);
-                const bool got = __all_sync(0xffffffffu, mbar_wait(&m->s_full[b], u, abort, wlim));
+                const bool got = warp_wait(&m->s_full[b], u, abort, wlim);
                 float sv[64];
                 float mx = -INFINITY;
                 if (got) {
@@ -740,35 +778,31 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     f0 += p0;
                     f1 += p1;
                 }
-                // P buffer b is free once P.V of block blk-2 completed
-                ok = __all_sync(0xffffffffu, mbar_wait(&m->p_empty[b], u ^ 1, abort, wlim));
+                // the weight buffer is free, and O at rest, once P.V of the block before completed
+                ok = warp_wait(&m->p_empty, (blk & 1) ^ 1, abort, wlim);
                 const bool need = rescale && k > sg.k0;
                 float f = 1.0f;
                 if (need) f = fast_exp2(mrun - muse);
                 if (ok && __any_sync(0xffffffffu, need)) {
-                    // O must be stable: P.V of the block before has completed.  TMEM loads and
-                    // stores are warp-wide: lanes whose row keeps its max scale by 1.
-                    ok = __all_sync(0xffffffffu, mbar_wait(&m->p_empty[b ^ 1], ((blk - 1) >> 1) & 1, abort, wlim));
-                    if (ok) {
-                        tc_fence_after();
+                    // TMEM loads and stores are warp-wide: lanes whose row keeps its max scale by 1
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 256; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tm_o + lane_off + c0, o);
-                            tmem_wait_ld();
+                    for (int c0 = 0; c0 < 256; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tm_o + lane_off + c0, o);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st32(tm_o + lane_off + c0, o);
-                        }
-                        tmem_wait_st();
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(tm_o + lane_off + c0, o);
                     }
+                    tmem_wait_st();
                 }
                 lrun = lrun * f + (r0 + r1);
                 lfull = lfull * f + (f0 + f1);
                 mrun = muse;
                 if (ok) {
                     // P row hl, chunk of this half: eight 16-byte pieces of a 128-byte row (128-byte swizzle)
-                    uint8_t* prow = s_p + b * Cfg::P_BYTES + half * 8192 + hl * 128;
+                    uint8_t* prow = s_p + half * 8192 + hl * 128;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         *reinterpret_cast<uint4*>(prow + ((((uint32_t)q) ^ (uint32_t)(hl & 7)) << 4)) =
@@ -776,14 +810,14 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_leader(&m->p_full[b], crank);
+                    if (lane == 0) arrive_leader(&m->p_full, crank);
                 } else {
                     *abort = 1;          // the vote of the next barrier ends the loop in every warp
                 }
             }
             // ------------------------------------------------------------ epilogue of a segment
             // the row's sums: this lane's positions plus the partner lane's
-            const bool ofull = ok && mbar_wait(&m->o_full, ns & 1, abort, wlim);
+            const bool ofull = ok && warp_wait(&m->o_full, ns & 1, abort, wlim);
             if (!named_bar_and(1, 128, ofull)) {
                 ok = false;
                 break;
@@ -798,6 +832,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             const int64_t row = (int64_t)sg.row0 + rr;
             if (sg.part == 0) {
                 const float inv = empty ? 0.0f : 1.0f / ltot;
+#pragma unroll 1
                 for (int c0 = 0; c0 < 256; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(tm_o + lane_off + c0, o);
@@ -820,6 +855,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 uint8_t* sl = p.part + Cfg::HEAD_BYTES +
                               ((int64_t)(2 * pair + (sg.part == 1 ? 1 : 0)) * 2 + crank) * Cfg::PART_BYTES;
                 float* od = reinterpret_cast<float*>(sl) + hl * 512;
+#pragma unroll 1
                 for (int c0 = 0; c0 < 256; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(tm_o + lane_off + c0, o);
@@ -849,7 +885,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     if (m->abort)
         for (int i = 0; i < 100; ++i) __nanosleep(10000);
     cluster_sync();   // no remote access may target an exited CTA, and no MMA may read a freed tile
-    if (warp == Cfg::MMA_WARP) {
+    if (warp == Cfg::QK_WARP) {
         tc_fence_after();
         tmem_dealloc_2cta(tmem_base, Cfg::TMEM_COLS);
     }

@@ -108,6 +108,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// The same without suspension (test_wait), for waits on a kernel's critical path: a
+// thread that try_wait has suspended is woken late.  The loop is a function of its
+// own, shared by all call sites: in a kernel of many roles the instruction cache is
+// scarce, and an answer that is there at once needs no loop.
+static __device__ __noinline__ bool mbar_spin_loop(uint32_t a, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_test_wait(a, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer() - t0 > limit_ns) return false;
+    }
+}
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    const uint32_t a = smem_u32(bar);
+    return mbar_test_wait(a, parity) || mbar_spin_loop(a, parity, abort, limit_ns);
+}
+
 // ------------------------------------------------------------------ grid dependencies (programmatic launch)
 // Waits until the grids this one depends on have completed and their memory
 // operations are visible (returns at once when launched without a dependency).
@@ -164,11 +183,12 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, u
 }
 // Two-CTA form of the tiled load (cta_group::2): the bytes land in this CTA and are
 // counted on an mbarrier of either CTA of the pair (a shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y) {
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y,
+                                                 int z) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 // 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16).
