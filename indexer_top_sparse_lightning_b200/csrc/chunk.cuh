@@ -22,12 +22,12 @@
 //       2k + c), nine K-chunks of 64 columns;
 //   O += P.V: M = 128 rows, N = 256 value columns twice (CTA c holds columns
 //       128c.. and 256 + 128c.. of both pages), K = 128 positions.
-// Keys and values have a ring each (a whole block of keys in three groups of
-// 64 rows x 192 columns, a whole block of values in four groups of 32 rows x 256
-// columns of the pair's 512), a loading warp each and an issuing warp each: one
+// Keys and values have a ring each (a block of keys in three groups of 64 rows x
+// 192 columns; of values, three groups of 32 rows x 256 of the pair's 512 columns,
+// four make a block), a loading warp each and an issuing warp each: one
 // warp cannot issue a block's 52 MMAs and wait for their operands in the time
 // that the MMAs take.  The issuing warps run ahead of one another as far as the
-// two score buffers and the one weight buffer allow, across tiles too, so the
+// two score buffers and the two weight buffers allow, across tiles too, so the
 // softmax of one block runs under the products of its neighbours.  Every group is
 // one or two copies (the tensor maps have the 64-column chunks of a row as their
 // outermost dimension), counted for both CTAs on CTA 0's barriers (the two-CTA
@@ -47,14 +47,14 @@
 // tokens that see one have a non-finite score already).  Only the slots at the
 // tile's causal edge take this path (the "fixer" warp).
 //
-// Roles per CTA (320 threads):
-//   warps 0-3   softmax and epilogue (thread L <-> TMEM lane L: row 64c + L%64,
-//               positions 64*(L/64).. of a block)
-//   warp 4      TMEM allocation; CTA 0: issues the score MMAs
-//   warp 5      CTA 0: issues the value MMAs
-//   warps 6, 7  loads of keys, of values
-//   warp 8      segments (runs of one tile's blocks) and the loads of Q
-//   warp 9      fixer
+// Roles per CTA (448 threads):
+//   warps 0-7   softmax and epilogue (warps w and w + 4 share TMEM lanes 32(w%4)..;
+//               lane L: row 64c + L%64, positions 64*(L/64).. of a block)
+//   warp 8      TMEM allocation; CTA 0: issues the score MMAs
+//   warp 9      CTA 0: issues the value MMAs
+//   warps 10, 11  loads of keys, of values
+//   warp 12     segments (runs of one tile's blocks) and the loads of Q
+//   warp 13     fixer
 #pragma once
 #include "common.h"
 #include "fp8row.cuh"
@@ -70,19 +70,21 @@ struct ChunkCfg {
     static constexpr int KGROUPS = 3;                   // groups of a block's keys: 64 rows x 3 chunks
     static constexpr int KGROUP = 3 * 8192;
     static constexpr int VGROUPS = 4;                   // groups of a block's values: 32 rows x 4 chunks (this CTA's)
+    static constexpr int VRING = 3;                     // groups that are kept
     static constexpr int VGROUP = 4 * 4096;
     static constexpr int Q_BYTES = KCH * 64 * 128;      // this CTA's 64 rows
     static constexpr int P_BYTES = 64 * BLOCK * 2;      // [64 rows x 128 positions] bf16: two 64-position chunks
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
-    static constexpr int OFF_K = OFF_P + P_BYTES;
+    static constexpr int OFF_K = OFF_P + 2 * P_BYTES;
     static constexpr int OFF_V = OFF_K + KGROUPS * KGROUP;
-    static constexpr int OFF_XM = OFF_V + VGROUPS * VGROUP;   // partner exchange, two buffers of 128 floats
-    static constexpr int OFF_MISC = OFF_XM + 2 * 128 * 4;
+    static constexpr int OFF_XM = OFF_V + VRING * VGROUP;   // exchange between the threads of a row
+    static constexpr int OFF_MISC = OFF_XM + 256 * 4;
     static constexpr int MISC_BYTES = 1024;
     static constexpr int SMEM = 1024 + OFF_MISC + MISC_BYTES;
-    static constexpr int THREADS = 320;
-    static constexpr int QK_WARP = 4, PV_WARP = 5, KEY_WARP = 6, VALUE_WARP = 7, SEG_WARP = 8, FIX_WARP = 9;
+    static constexpr int SOFTMAX_WARPS = 8;
+    static constexpr int QK_WARP = 8, PV_WARP = 9, KEY_WARP = 10, VALUE_WARP = 11, SEG_WARP = 12, FIX_WARP = 13;
+    static constexpr int THREADS = 448;
     static constexpr int NSEG = 4;                      // segment ring
     static constexpr int TMEM_COLS = 512;               // O: [0, 256), two score buffers of 64 from column 256
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, BLOCK, false, false);
@@ -128,12 +130,12 @@ struct ChunkSeg {
 struct ChunkMisc {
     uint64_t k_full[ChunkCfg::KGROUPS];   // (CTA 0) the key group is ready in both CTAs
     uint64_t k_empty[ChunkCfg::KGROUPS];  // its MMAs have completed
-    uint64_t v_full[ChunkCfg::VGROUPS];   // (CTA 0) the value group is ready in both CTAs
-    uint64_t v_empty[ChunkCfg::VGROUPS];
-    uint64_t v_land[ChunkCfg::VGROUPS];   // the group has landed, for the fixer to look at
+    uint64_t v_full[ChunkCfg::VRING];   // (CTA 0) the value group is ready in both CTAs
+    uint64_t v_empty[ChunkCfg::VRING];
+    uint64_t v_land[ChunkCfg::VRING];   // the group has landed, for the fixer to look at
     uint64_t q_full;                      // (CTA 0) Q of both CTAs
     uint64_t q_empty;
-    uint64_t s_full[2], s_empty[2], p_full, p_empty;
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t o_full, o_empty, drain[2];
     uint64_t seg_full[ChunkCfg::NSEG], seg_empty[ChunkCfg::NSEG];
     ChunkSeg seg[ChunkCfg::NSEG];
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             mbar_init(&m->k_full[i], 1);    // CTA 0's loader, for both CTAs
             mbar_init(&m->k_empty[i], 1);
         }
-        for (int i = 0; i < Cfg::VGROUPS; ++i) {
+        for (int i = 0; i < Cfg::VRING; ++i) {
             mbar_init(&m->v_full[i], 2);    // two by CTA 0's loader, or one by each CTA's fixer
             mbar_init(&m->v_empty[i], 1);
             mbar_init(&m->v_land[i], 1);
@@ -283,16 +285,16 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         mbar_init(&m->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->s_full[i], 1);
-            mbar_init(&m->s_empty[i], 8);   // one arrival per softmax warp of both CTAs
+            mbar_init(&m->s_empty[i], 2 * Cfg::SOFTMAX_WARPS);   // those of both CTAs
+            mbar_init(&m->p_full[i], 2 * Cfg::SOFTMAX_WARPS);
+            mbar_init(&m->p_empty[i], 1);
             mbar_init(&m->drain[i], 1);
         }
-        mbar_init(&m->p_full, 8);
-        mbar_init(&m->p_empty, 1);
         mbar_init(&m->o_full, 1);
-        mbar_init(&m->o_empty, 8);
+        mbar_init(&m->o_empty, 2 * Cfg::SOFTMAX_WARPS);
         for (int i = 0; i < Cfg::NSEG; ++i) {
             mbar_init(&m->seg_full[i], 1);
-            mbar_init(&m->seg_empty[i], crank == 0 ? 9 : 7);   // softmax, loading and fixer warps; CTA 0: the issuers too
+            mbar_init(&m->seg_empty[i], Cfg::SOFTMAX_WARPS + (crank == 0 ? 5 : 3));   // loading and fixer warps; CTA 0: the issuers too
         }
         m->abort = 0;
         m->start_b = -1;
@@ -482,8 +484,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         auto load_values = [&](const ChunkBlock& cb, int id0, int id1) -> bool {
 #pragma unroll 1
             for (int g = 0; g < cb.ngroups; ++g, ++n) {
-                const uint32_t r = n % Cfg::VGROUPS;
-                if (!elected_wait(el, &m->v_empty[r], ((n / Cfg::VGROUPS) & 1) ^ 1, abort, wlim)) return false;
+                const uint32_t r = n % Cfg::VRING;
+                if (!elected_wait(el, &m->v_empty[r], ((n / Cfg::VRING) & 1) ^ 1, abort, wlim)) return false;
                 const int id = g < 2 ? id0 : id1;
                 const bool fix = g >= cb.fix_from;
                 uint8_t* dst = s_v + r * Cfg::VGROUP;
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 const ChunkBlock cb = chunk_block(sg, k);
                 n += cb.fix_from;
                 for (int g = cb.fix_from; ok && g < cb.ngroups; ++g, ++n) {
-                    const uint32_t r = n % Cfg::VGROUPS;
+                    const uint32_t r = n % Cfg::VRING;
                     ok = warp_wait(&m->v_land[r], (phase >> r) & 1, abort, wlim);
                     if (!ok) break;
                     phase ^= 1u << r;
@@ -622,13 +624,12 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
 #pragma unroll 1
                 for (int g = 0; g < Cfg::KGROUPS; ++g) {
                     if (!elected_wait(el, &m->k_full[g], blk & 1, abort, wlim)) return false;
-#pragma unroll 1
-                    for (int kb = 3 * g; kb < 3 * g + 3; ++kb)
 #pragma unroll
-                        for (int k16 = 0; k16 < 4; ++k16)
-                            if (el)
-                                umma_bf16_2cta(d, q_desc + (kb * 512 + k16 * 2), k_desc + (kb * 512 + k16 * 2), Cfg::IDESC_QK,
-                                               (kb | k16) != 0);
+                    for (int j = 0; j < 12; ++j)
+                        if (el) {
+                            const uint32_t off = g * 1536 + (j >> 2) * 512 + (j & 3) * 2;
+                            umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::IDESC_QK, (g | j) != 0);
+                        }
                     if (el) umma_commit_2cta(&m->k_empty[g], 3);
                 }
                 if (el) umma_commit_2cta(&m->s_full[blk & 1], 3);
@@ -636,24 +637,25 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 return true;
             };
             auto issue_pv = [&](int ngroups, bool first, bool last) -> bool {
-                if (!elected_wait(el, &m->p_full, blk & 1, abort, wlim)) return false;
+                if (!elected_wait(el, &m->p_full[blk & 1], (blk >> 1) & 1, abort, wlim)) return false;
                 tc_fence_after();
+                const uint64_t pd = p_desc + (blk & 1) * (Cfg::P_BYTES / 16);
 #pragma unroll 1
                 for (int g = 0; g < ngroups; ++g) {
-                    const uint32_t r = n % Cfg::VGROUPS;
-                    if (!elected_wait(el, &m->v_full[r], (n / Cfg::VGROUPS) & 1, abort, wlim)) return false;
+                    const uint32_t r = n % Cfg::VRING;
+                    if (!elected_wait(el, &m->v_full[r], (n / Cfg::VRING) & 1, abort, wlim)) return false;
                     const uint64_t vd = v_desc + r * (Cfg::VGROUP / 16);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int s16 = 0; s16 < 2; ++s16)
                             if (el)        // A = P [64 rows x 16 positions] K-major
-                                umma_bf16_2cta(tm_o + h * 128, p_desc + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
+                                umma_bf16_2cta(tm_o + h * 128, pd + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
                                                vd + (h * 512 + s16 * 128), Cfg::IDESC_PV, g > 0 || s16 > 0 || !first);
                     if (el) umma_commit_2cta(&m->v_empty[r], 3);
                     ++n;
                 }
-                if (el) umma_commit_2cta(&m->p_empty, 3);
+                if (el) umma_commit_2cta(&m->p_empty[blk & 1], 3);
                 if (last && el) umma_commit_2cta(&m->o_full, 3);
                 return true;
             };
@@ -686,20 +688,35 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax + epilogue
-        const int L = threadIdx.x;                   // TMEM lane
+        // Four threads share a row: positions 64 * half + 32 * part .. of a block each, and 128
+        // value columns each in the end.
+        const int L = threadIdx.x & 127;             // TMEM lane
+        const int part = threadIdx.x >> 7;
         const int hl = L & 63;                       // row of this CTA's 64
-        const int half = L >> 6;                     // positions 64*half.. of a block; value columns of this half
+        const int half = L >> 6;
         const int rr = 64 * (int)crank + hl;         // row of the tile
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        auto col_of = [&](int c0) { return c0 < 128 ? 128 * half + c0 : 256 + 128 * half + (c0 - 128); };
+        const int p0 = 64 * half + 32 * part;        // first position of this thread in a block
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tm_mine = tm_o + lane_off + 128 * part;       // O: columns 256 * part + 128 * half ..
+        const int col0 = 256 * part + 128 * half;
+        // the row's value of all four threads combined; `x` of every thread is out before any is read
+        auto exchange = [&](float x, float (&of)[4]) {
+            s_xm[128 * part + L] = x;
+            named_bar_sync(1, 256);
+            of[0] = s_xm[hl];
+            of[1] = s_xm[hl + 64];
+            of[2] = s_xm[hl + 128];
+            of[3] = s_xm[hl + 192];
+            named_bar_sync(1, 256);
+        };
         uint32_t blk = 0;
         bool ok = true;
-        // Every exit decision of these 128 threads is taken together (votes carried
+        // Every exit decision of these 256 threads is taken together (votes carried
         // by named barriers), so the named barriers always match.
         for (int ns = 0;; ++ns) {
             const int sr = ns % Cfg::NSEG;
             const bool there = warp_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim);
-            ok = named_bar_and(1, 128, ok && there);
+            ok = named_bar_and(1, 256, ok && there);
             if (!ok) break;
             const ChunkSeg sg = m->seg[sr];
             __syncwarp();
@@ -720,159 +737,149 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             bool next_ok = page_ok(sg.k0);
             float mrun = -INFINITY, lrun = 0.0f, lfull = 0.0f;
             for (int k = sg.k0; k < sg.k1; ++k, ++blk) {
-                const int b = blk & 1;
-                const uint32_t u = (blk >> 1) & 1;
+                const uint32_t b = blk & 1, u = (blk >> 1) & 1;
                 const bool this_ok = next_ok;
                 if (k + 1 < sg.k1) next_ok = page_ok(k + 1);
-                const bool got = warp_wait(&m->s_full[b], u, abort, wlim);
-                float sv[64];
+                const bool got = ok && warp_wait(&m->s_full[b], u, abort, wlim);
+                float sv[32];
                 float mx = -INFINITY;
                 if (got) {
                     tc_fence_after();
-                    uint32_t a[32], a2[32];
-                    tmem_ld32(tm_s + lane_off + b * 64, a);
-                    tmem_ld32(tm_s + lane_off + b * 64 + 32, a2);
+                    uint32_t a[32];
+                    tmem_ld32(tm_s + lane_off + b * 64 + 32 * part, a);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_leader(&m->s_empty[b], crank);
-                    int vis = see - (k * Cfg::BLOCK + 64 * half);     // positions of this half that the row sees
-                    if (!this_ok) vis = 0;
-                    if (__all_sync(0xffffffffu, vis >= 64)) {
+                    // positions of this thread that the row sees
+                    const int vis = this_ok ? see - (k * Cfg::BLOCK + p0) : 0;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            sv[i] = __uint_as_float(a[i]) * p.scale_log2;
-                            sv[32 + i] = __uint_as_float(a2[i]) * p.scale_log2;
-                            mx = fmaxf(mx, fmaxf(sv[i], sv[32 + i]));
-                        }
-                    } else {
+                    for (int i = 0; i < 32; ++i) sv[i] = __uint_as_float(a[i]) * p.scale_log2;
+                    if (!__all_sync(0xffffffffu, vis >= 32))
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            sv[i] = i < vis ? __uint_as_float(a[i]) * p.scale_log2 : -INFINITY;
-                            sv[32 + i] = 32 + i < vis ? __uint_as_float(a2[i]) * p.scale_log2 : -INFINITY;
-                            mx = fmaxf(mx, fmaxf(sv[i], sv[32 + i]));
-                        }
-                    }
+                        for (int i = 0; i < 32; ++i) sv[i] = i < vis ? sv[i] : -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, sv[i]);
                 }
-                // the row's other 64 positions are in lane L^64 (two exchange buffers, so the next
-                // block's write cannot meet this read)
-                float* xm = s_xm + b * 128;
-                xm[L] = mx;
-                ok = named_bar_and(1, 128, ok && got);
-                if (!ok) break;
-                const float mnew = fmaxf(mrun, fmaxf(mx, xm[L ^ 64]));
-                const bool rescale = mnew > mrun + 8.0f;      // identical in both lanes of a row
-                const float muse = rescale ? mnew : mrun;
-                const bool none = muse == -INFINITY;
-                uint32_t pk[32];
+                // The reference maximum stays while no thread's scores are above it by more than 2^8
+                // (one barrier, no exchange); otherwise every row takes its new maximum.
+                float muse = mrun;
+                bool rescale = false;
+                if (!named_bar_and(1, 256, ok && got && !(mx > mrun + 8.0f))) {
+                    ok = named_bar_and(1, 256, ok && got);
+                    if (!ok) break;
+                    float of[4];
+                    exchange(mx, of);
+                    const float mnew = fmaxf(mrun, fmaxf(fmaxf(of[0], of[1]), fmaxf(of[2], of[3])));
+                    rescale = mnew > mrun + 8.0f;      // identical in the four threads of a row
+                    if (rescale) muse = mnew;
+                }
+                const float base = muse == -INFINITY ? 0.0f : muse;   // (nothing seen yet: 2^-inf)
+                uint32_t pk[16];
                 float r0 = 0.0f, r1 = 0.0f, f0 = 0.0f, f1 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float p0 = none ? 0.0f : fast_exp2(sv[2 * i] - muse);
-                    const float p1 = none ? 0.0f : fast_exp2(sv[2 * i + 1] - muse);
-                    pk[i] = pack_bf16(p0, p1);
+                for (int i = 0; i < 16; ++i) {
+                    const float e0 = fast_exp2(sv[2 * i] - base);
+                    const float e1 = fast_exp2(sv[2 * i + 1] - base);
+                    pk[i] = pack_bf16(e0, e1);
                     // O is divided by the sum of the bf16 weights that the MMA multiplies (their
                     // roundings cancel in part); lse takes the sum before rounding
                     r0 += __uint_as_float(pk[i] << 16);
                     r1 += __uint_as_float(pk[i] & 0xFFFF0000u);
-                    f0 += p0;
-                    f1 += p1;
+                    f0 += e0;
+                    f1 += e1;
                 }
-                // the weight buffer is free, and O at rest, once P.V of the block before completed
-                ok = warp_wait(&m->p_empty, (blk & 1) ^ 1, abort, wlim);
-                const bool need = rescale && k > sg.k0;
+                // weight buffer b is free once P.V of block blk - 2 completed
+                ok = warp_wait(&m->p_empty[b], u ^ 1, abort, wlim);
                 float f = 1.0f;
+                const bool need = rescale && k > sg.k0;
                 if (need) f = fast_exp2(mrun - muse);
                 if (ok && __any_sync(0xffffffffu, need)) {
-                    // TMEM loads and stores are warp-wide: lanes whose row keeps its max scale by 1
-                    tc_fence_after();
+                    // O at rest: P.V of the block before has completed.  TMEM loads and stores are
+                    // warp-wide: lanes whose row keeps its max scale by 1.
+                    ok = warp_wait(&m->p_empty[b ^ 1], ((blk - 1) >> 1) & 1, abort, wlim);
+                    if (ok) {
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < 256; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tm_o + lane_off + c0, o);
-                        tmem_wait_ld();
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tm_mine + c0, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(tm_o + lane_off + c0, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(tm_mine + c0, o);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
                 }
                 lrun = lrun * f + (r0 + r1);
                 lfull = lfull * f + (f0 + f1);
                 mrun = muse;
                 if (ok) {
-                    // P row hl, chunk of this half: eight 16-byte pieces of a 128-byte row (128-byte swizzle)
-                    uint8_t* prow = s_p + half * 8192 + hl * 128;
+                    // P row hl, chunk of this half: four 16-byte pieces of a 128-byte row (128-byte swizzle)
+                    uint8_t* prow = s_p + b * Cfg::P_BYTES + half * 8192 + hl * 128;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        *reinterpret_cast<uint4*>(prow + ((((uint32_t)q) ^ (uint32_t)(hl & 7)) << 4)) =
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(prow + (((uint32_t)(4 * part + q) ^ (uint32_t)(hl & 7)) << 4)) =
                             make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_leader(&m->p_full, crank);
+                    if (lane == 0) arrive_leader(&m->p_full[b], crank);
                 } else {
                     *abort = 1;          // the vote of the next barrier ends the loop in every warp
                 }
             }
             // ------------------------------------------------------------ epilogue of a segment
-            // the row's sums: this lane's positions plus the partner lane's
             const bool ofull = ok && warp_wait(&m->o_full, ns & 1, abort, wlim);
-            if (!named_bar_and(1, 128, ofull)) {
-                ok = false;
-                break;
-            }
-            s_xm[L] = lrun;
-            s_xm[128 + L] = lfull;
-            named_bar_sync(1, 128);
-            const float ltot = lrun + s_xm[L ^ 64];
-            const float lft = lfull + s_xm[128 + (L ^ 64)];
+            ok = named_bar_and(1, 256, ofull);
+            if (!ok) break;
+            float of[4];
+            exchange(lrun, of);
+            const float ltot = (of[0] + of[1]) + (of[2] + of[3]);
+            exchange(lfull, of);
+            const float lft = (of[0] + of[1]) + (of[2] + of[3]);
             tc_fence_after();
             const bool empty = ltot == 0.0f;   // the row saw nothing here
             const int64_t row = (int64_t)sg.row0 + rr;
-            if (sg.part == 0) {
-                const float inv = empty ? 0.0f : 1.0f / ltot;
+            const float inv = empty ? 0.0f : 1.0f / ltot;
+            uint8_t* sl = p.part + Cfg::HEAD_BYTES +
+                          ((int64_t)(2 * pair + (sg.part == 1 ? 1 : 0)) * 2 + crank) * Cfg::PART_BYTES;
 #pragma unroll 1
-                for (int c0 = 0; c0 < 256; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tm_o + lane_off + c0, o);
-                    tmem_wait_ld();
-                    if (real) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDv + col_of(c0));
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(tm_mine + c0, o);
+                tmem_wait_ld();
+                if (!real) continue;
+                if (empty)                     // O was never written, or holds 0 x anything
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            float v[8];
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                if (sg.part == 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDv + col0 + c0);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] = empty ? 0.0f : __uint_as_float(o[i + e]) * inv;
-                            dst[i / 8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                    pack_bf16(v[6], v[7]));
-                        }
+                    for (int i = 0; i < 32; i += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[i + e]) * inv;
+                        dst[i / 8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                pack_bf16(v[6], v[7]));
                     }
-                }
-                if (half == 0 && real && p.lse)
-                    p.lse[row] = empty ? -INFINITY : (mrun + log2f(lft)) * 0.69314718055994531f;
-            } else {
-                uint8_t* sl = p.part + Cfg::HEAD_BYTES +
-                              ((int64_t)(2 * pair + (sg.part == 1 ? 1 : 0)) * 2 + crank) * Cfg::PART_BYTES;
-                float* od = reinterpret_cast<float*>(sl) + hl * 512;
-#pragma unroll 1
-                for (int c0 = 0; c0 < 256; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tm_o + lane_off + c0, o);
-                    tmem_wait_ld();
-                    if (real)
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<float*>(sl) + hl * 512 + col0 + c0);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            __stcg(reinterpret_cast<uint4*>(od + col_of(c0) + i),
-                                   empty ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+                    for (int i = 0; i < 32; i += 4) __stcg(dst + i / 4, make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
                 }
-                if (half == 0 && real)
+            }
+            if (half == 0 && part == 0 && real) {
+                if (sg.part != 0)
                     __stcg(reinterpret_cast<float4*>(sl + Cfg::PART_O) + hl,
                            make_float4(empty ? -INFINITY : mrun, ltot, lft, 0.0f));
+                else if (p.lse)
+                    p.lse[row] = empty ? -INFINITY : (mrun + log2f(lft)) * 0.69314718055994531f;
             }
             // O has been read: the next segment's first P.V may overwrite it
             tc_fence_before();
-            named_bar_sync(1, 128);
+            __syncwarp();
             if (lane == 0) arrive_leader(&m->o_empty, crank);
         }
         if (!ok) *abort = 1;
