@@ -109,7 +109,7 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     }
     CUtensorMap tm_q, tm_k, tm_v;
     if (!rows_map(&tm_q, at->q, (uint64_t)batch->num_tokens * at->H, 64, ChunkCfg::KCH) ||
-        !rows_map(&tm_k, rows, nrows, 64, 3) || !rows_map(&tm_v, rows, nrows, 32, 2))
+        !rows_map(&tm_k, rows, nrows, 64, 3) || !rows_map(&tm_v, rows, nrows, 32, 4))
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");
     if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(&chunk_attn_kernel), ChunkCfg::SMEM))
         return fail(DSA_ERR_CUDA, "shared memory attribute", e);

@@ -21,7 +21,8 @@
 //   S = Q.K^T: M = 128 rows (64 per CTA), N = 128 positions (CTA c holds page
 //       2k + c), nine K-chunks of 64 columns;
 //   O += P.V: M = 128 rows, N = 256 value columns twice (CTA c holds columns
-//       128c.. and 256 + 128c.. of both pages), K = 128 positions.
+//       256c.. of both pages; MMA h takes 128 of them from each CTA, columns
+//       128h.. and 256 + 128h..), K = 128 positions.
 // Keys and values have a ring each (a block of keys in three groups of 64 rows x
 // 192 columns; of values, three groups of 32 rows x 256 of the pair's 512 columns,
 // four make a block), a loading warp each and an issuing warp each: one
@@ -85,6 +86,10 @@ struct ChunkCfg {
     static constexpr int SOFTMAX_WARPS = 8;
     static constexpr int QK_WARP = 8, PV_WARP = 9, KEY_WARP = 10, VALUE_WARP = 11, SEG_WARP = 12, FIX_WARP = 13;
     static constexpr int THREADS = 448;
+    // A row's reference maximum is replaced once a score exceeds it by 2^32: weights and sums
+    // are floating point, so a lower reference costs no precision, and 2^32 (2^52 for the sums of
+    // a million weights) is far from fp32's range.  A replacement waits for the P.V in flight.
+    static constexpr float LAZY = 32.0f;
     static constexpr int NSEG = 4;                      // segment ring
     static constexpr int TMEM_COLS = 512;               // O: [0, 256), two score buffers of 64 from column 256
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, BLOCK, false, false);
@@ -132,6 +137,7 @@ struct ChunkMisc {
     uint64_t k_empty[ChunkCfg::KGROUPS];  // its MMAs have completed
     uint64_t v_full[ChunkCfg::VRING];   // (CTA 0) the value group is ready in both CTAs
     uint64_t v_empty[ChunkCfg::VRING];
+    uint64_t v_peer[ChunkCfg::VRING];     // (CTA 0) CTA 1's fixer is done with the group
     uint64_t v_land[ChunkCfg::VRING];   // the group has landed, for the fixer to look at
     uint64_t q_full;                      // (CTA 0) Q of both CTAs
     uint64_t q_empty;
@@ -277,7 +283,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             mbar_init(&m->k_empty[i], 1);
         }
         for (int i = 0; i < Cfg::VRING; ++i) {
-            mbar_init(&m->v_full[i], 2);    // two by CTA 0's loader, or one by each CTA's fixer
+            mbar_init(&m->v_full[i], 1);    // CTA 0's loader or fixer, for both CTAs
+            mbar_init(&m->v_peer[i], 1);
             mbar_init(&m->v_empty[i], 1);
             mbar_init(&m->v_land[i], 1);
         }
@@ -458,7 +465,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         // test hook: the second CTA never loads
         bool ok = !(crank == 1 && (m->inject & 4u));
         bool bad = false;
-        uint32_t n = 0;                    // blocks (keys) or groups (values) so far
+        uint32_t r = 0, ph = 1;            // group of the ring and the parity that its `empty` waits for
         const uint32_t k_lead = mapa_shared(smem_u32(&m->k_full[0]), 0), v_lead = mapa_shared(smem_u32(&m->v_full[0]), 0);
         ChunkSeg sg = {};
         const int32_t* table = nullptr;
@@ -472,22 +479,41 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             // a page that nobody sees is not loaded: its scores are replaced whatever they are
             const uint32_t bytes = (uint32_t)Cfg::KGROUP * ((id0 >= 0) + (id1 >= 0));
             const bool mine = el && id >= 0;
+            const int y = id * kPage;
 #pragma unroll 1
             for (int g = 0; g < Cfg::KGROUPS; ++g) {
-                if (!elected_wait(el, &m->k_empty[g], (n & 1) ^ 1, abort, wlim)) return false;
+                if (!elected_wait(el, &m->k_empty[g], ph, abort, wlim)) return false;
                 if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[g], bytes);
-                if (mine) tma_load_3d_pair(s_k + g * Cfg::KGROUP, &tm_k, k_lead + 8 * g, 0, id * kPage, 3 * g);
+                if (mine) tma_load_3d_pair(s_k + g * Cfg::KGROUP, &tm_k, k_lead + 8 * g, 0, y, 3 * g);
             }
-            ++n;
+            ph ^= 1;
             return true;
         };
-        auto load_values = [&](const ChunkBlock& cb, int id0, int id1) -> bool {
+        auto next_group = [&]() {
+            if (++r == Cfg::VRING) {
+                r = 0;
+                ph ^= 1;
+            }
+        };
+        // Four groups of 32 positions, both pages good, nothing for the fixer.
+        auto load_values = [&](int id0, int id1) -> bool {
 #pragma unroll 1
-            for (int g = 0; g < cb.ngroups; ++g, ++n) {
-                const uint32_t r = n % Cfg::VRING;
-                if (!elected_wait(el, &m->v_empty[r], ((n / Cfg::VRING) & 1) ^ 1, abort, wlim)) return false;
+            for (int g = 0; g < Cfg::VGROUPS; ++g) {
+                if (!elected_wait(el, &m->v_empty[r], ph, abort, wlim)) return false;
+                if (crank == 0 && el) mbar_arrive_expect_tx(&m->v_full[r], 2 * Cfg::VGROUP);
+                const int y = (g < 2 ? id0 : id1) * kPage + 32 * (g & 1);
+                if (el) tma_load_3d_pair(s_v + r * Cfg::VGROUP, &tm_v, v_lead + 8 * r, 0, y, 4 * (int)crank);
+                next_group();
+            }
+            return true;
+        };
+        // The same at the causal edge (the groups that the fixer looks at first), or with a bad
+        // page: all groups of such a block go through the fixer's hands.
+        auto load_values_edge = [&](const ChunkBlock& cb, int id0, int id1) -> bool {
+#pragma unroll 1
+            for (int g = 0; g < cb.ngroups; ++g, next_group()) {
+                if (!elected_wait(el, &m->v_empty[r], ph, abort, wlim)) return false;
                 const int id = g < 2 ? id0 : id1;
-                const bool fix = g >= cb.fix_from;
                 uint8_t* dst = s_v + r * Cfg::VGROUP;
                 if (id < 0) {              // a bad page id: zeros
                     for (int i = lane; i < Cfg::VGROUP / 16; i += 32)
@@ -495,26 +521,12 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                const int y = id * kPage + 32 * (g & 1), z = 2 * (int)crank;
                 if (!el) continue;
-                if (fix) {
-                    // this CTA's fixer looks at the rows before the MMAs may
-                    if (id >= 0) {
-                        mbar_arrive_expect_tx(&m->v_land[r], Cfg::VGROUP);
-                        tma_load_3d(dst, &tm_v, &m->v_land[r], 0, y, z);
-                        tma_load_3d(dst + Cfg::VGROUP / 2, &tm_v, &m->v_land[r], 0, y, z + 4);
-                    } else {
-                        mbar_arrive(&m->v_land[r]);
-                    }
-                } else if (id >= 0) {
-                    if (crank == 0) {
-                        mbar_arrive_expect_tx(&m->v_full[r], 2 * Cfg::VGROUP);
-                        mbar_arrive(&m->v_full[r]);
-                    }
-                    tma_load_3d_pair(dst, &tm_v, v_lead + 8 * r, 0, y, z);
-                    tma_load_3d_pair(dst + Cfg::VGROUP / 2, &tm_v, v_lead + 8 * r, 0, y, z + 4);
+                if (id >= 0) {
+                    mbar_arrive_expect_tx(&m->v_land[r], Cfg::VGROUP);
+                    tma_load_3d(dst, &tm_v, &m->v_land[r], 0, id * kPage + 32 * (g & 1), 4 * (int)crank);
                 } else {
-                    arrive_leader(&m->v_full[r], crank);
+                    mbar_arrive(&m->v_land[r]);
                 }
             }
             return true;
@@ -539,7 +551,9 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     bad = bad || a0 == -2 || a1 == -2;
                     ok = load_keys(a0, a1);
                 } else {
-                    ok = load_values(chunk_block(sg, k), a0, a1);
+                    const ChunkBlock cb = chunk_block(sg, k);
+                    const bool plain = __all_sync(0xffffffffu, cb.fix_from == Cfg::VGROUPS && a0 >= 0 && a1 >= 0);
+                    ok = plain ? load_values(a0, a1) : load_values_edge(cb, a0, a1);
                 }
                 a0 = b0;
                 a1 = b1;
@@ -550,7 +564,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     } else if (warp == Cfg::FIX_WARP) {
         // ---------------------------------------------------------------- value rows at the causal edge
         bool ok = true;
-        uint32_t n = 0, phase = 0;         // groups so far; next phase of each land barrier
+        uint32_t n = 0, phase = 0, peer = 0;   // groups so far; next phase of each land and peer barrier
         for (int ns = 0; ok; ++ns) {
             const int sr = ns % Cfg::NSEG;
             if (!warp_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim)) {
@@ -561,10 +575,31 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->seg_empty[sr]);
             if (sg.b < 0) break;
+            // the loader's rule for the blocks that it hands over: lanes 2i and 2i + 1 look at the
+            // pages of block kb + i
+            const int32_t* table = p.block_table + (int64_t)sg.b * p.max_blocks;
+            int kb = sg.k0 - 16;
+            uint32_t good = 0;
+            auto pages_ok = [&](int k) -> bool {
+                if (k >= kb + 16) {
+                    kb = k;
+                    const int page = 2 * k + lane;
+                    bool fine = true;
+                    if (page < p.max_blocks && page * kPage < sg.see) {
+                        const int id = __ldg(table + page);
+                        fine = id >= 0 && id < p.num_blocks;
+                    }
+                    good = __ballot_sync(0xffffffffu, fine);
+                }
+                return ((good >> (2 * (k - kb))) & 3u) == 3u;
+            };
             for (int k = sg.k0; ok && k < sg.k1; ++k) {
                 const ChunkBlock cb = chunk_block(sg, k);
-                n += cb.fix_from;
-                for (int g = cb.fix_from; ok && g < cb.ngroups; ++g, ++n) {
+                if (cb.fix_from == Cfg::VGROUPS && pages_ok(k)) {
+                    n += Cfg::VGROUPS;
+                    continue;
+                }
+                for (int g = 0; ok && g < cb.ngroups; ++g, ++n) {
                     const uint32_t r = n % Cfg::VRING;
                     ok = warp_wait(&m->v_land[r], (phase >> r) & 1, abort, wlim);
                     if (!ok) break;
@@ -594,7 +629,14 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                         for (int q = 0; q < 32; ++q) *part(q) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_leader(&m->v_full[r], crank);
+                    // CTA 0's fixer hands the group over once both have looked at it
+                    if (crank == 1) {
+                        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&m->v_peer[r]), 0));
+                    } else {
+                        ok = warp_wait(&m->v_peer[r], (peer >> r) & 1, abort, wlim);
+                        peer ^= 1u << r;
+                        if (ok && lane == 0) mbar_arrive(&m->v_full[r]);
+                    }
                 }
             }
         }
@@ -615,7 +657,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             // V [16 positions x 128 columns per CTA] MN-major: 64-column chunks of 32 rows 4096 B
             // apart (LBO), 8-row groups 1024 B (SBO)
             const uint64_t v_desc = sdesc_sw128(smem_u32(s_v), 4096, 1024);
-            uint32_t blk = 0, n = 0;       // blocks and value groups so far
+            uint32_t blk = 0;              // blocks so far
+            uint32_t r = 0, ph = 0;        // group of the value ring and its parity
             auto issue_qk = [&](bool last) -> bool {
                 // scores of this buffer's block before have been read
                 if (!elected_wait(el, &m->s_empty[blk & 1], ((blk >> 1) & 1) ^ 1, abort, wlim)) return false;
@@ -642,8 +685,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 const uint64_t pd = p_desc + (blk & 1) * (Cfg::P_BYTES / 16);
 #pragma unroll 1
                 for (int g = 0; g < ngroups; ++g) {
-                    const uint32_t r = n % Cfg::VRING;
-                    if (!elected_wait(el, &m->v_full[r], (n / Cfg::VRING) & 1, abort, wlim)) return false;
+                    if (!elected_wait(el, &m->v_full[r], ph, abort, wlim)) return false;
                     const uint64_t vd = v_desc + r * (Cfg::VGROUP / 16);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -653,7 +695,10 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                                 umma_bf16_2cta(tm_o + h * 128, pd + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
                                                vd + (h * 512 + s16 * 128), Cfg::IDESC_PV, g > 0 || s16 > 0 || !first);
                     if (el) umma_commit_2cta(&m->v_empty[r], 3);
-                    ++n;
+                    if (++r == Cfg::VRING) {
+                        r = 0;
+                        ph ^= 1;
+                    }
                 }
                 if (el) umma_commit_2cta(&m->p_empty[blk & 1], 3);
                 if (last && el) umma_commit_2cta(&m->o_full, 3);
@@ -697,8 +742,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         const int rr = 64 * (int)crank + hl;         // row of the tile
         const int p0 = 64 * half + 32 * part;        // first position of this thread in a block
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tm_mine = tm_o + lane_off + 128 * part;       // O: columns 256 * part + 128 * half ..
-        const int col0 = 256 * part + 128 * half;
+        const uint32_t tm_mine = tm_o + lane_off + 128 * part;
+        const int col0 = 256 * half + 128 * part;    // first of this thread's value columns
         // the row's value of all four threads combined; `x` of every thread is out before any is read
         auto exchange = [&](float x, float (&of)[4]) {
             s_xm[128 * part + L] = x;
@@ -761,17 +806,17 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mx = fmaxf(mx, sv[i]);
                 }
-                // The reference maximum stays while no thread's scores are above it by more than 2^8
+                // The reference maximum stays while no thread's scores are above it by more than LAZY
                 // (one barrier, no exchange); otherwise every row takes its new maximum.
                 float muse = mrun;
                 bool rescale = false;
-                if (!named_bar_and(1, 256, ok && got && !(mx > mrun + 8.0f))) {
+                if (!named_bar_and(1, 256, ok && got && !(mx > mrun + Cfg::LAZY))) {
                     ok = named_bar_and(1, 256, ok && got);
                     if (!ok) break;
                     float of[4];
                     exchange(mx, of);
                     const float mnew = fmaxf(mrun, fmaxf(fmaxf(of[0], of[1]), fmaxf(of[2], of[3])));
-                    rescale = mnew > mrun + 8.0f;      // identical in the four threads of a row
+                    rescale = mnew > mrun + Cfg::LAZY;      // identical in the four threads of a row
                     if (rescale) muse = mnew;
                 }
                 const float base = muse == -INFINITY ? 0.0f : muse;   // (nothing seen yet: 2^-inf)
