@@ -68,7 +68,8 @@ size_t dsa_chunk_scratch_size(const dsa_batch* batch, const dsa_attn_inputs* at)
 dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, void* out, float* lse, void* status,
                           void* scratch, size_t scratch_bytes, void* stream) {
     ChunkPlan pl;
-    if (dsa_status st = plan_chunk(batch, at, dev_info(), pl)) return st;
+    const DevInfo di = dev_info();
+    if (dsa_status st = plan_chunk(batch, at, di, pl)) return st;
     if (!out || !aligned16(out) || !status || (reinterpret_cast<uintptr_t>(status) & 3u)) return DSA_ERR_INVALID_ARG;
     if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < pl.total) return DSA_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -133,12 +134,12 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     if (pl.pairs < 2) return DSA_OK;
     cudaLaunchConfig_t ccfg;
     memset(&ccfg, 0, sizeof ccfg);
-    ccfg.gridDim = dim3(pl.pairs - 1, ChunkCfg::ROWS / (ChunkCfg::COMBINE_THREADS / 32), 1);
+    ccfg.gridDim = dim3(2 * di.sms, 1, 1);
     ccfg.blockDim = dim3(ChunkCfg::COMBINE_THREADS, 1, 1);
     ccfg.stream = s;
     ccfg.attrs = attr;
     ccfg.numAttrs = 1;
-    if (cudaError_t e = cudaLaunchKernelEx(&ccfg, &chunk_combine_kernel, p)) return fail(DSA_ERR_CUDA, "merge launch", e);
+    if (cudaError_t e = cudaLaunchKernelEx(&ccfg, &chunk_combine_kernel, p, pl.pairs)) return fail(DSA_ERR_CUDA, "merge launch", e);
     return DSA_OK;
 }
 

@@ -100,10 +100,11 @@ struct ChunkCfg {
     static constexpr int64_t PART_BYTES = PART_O + 64 * 16;
     static constexpr int64_t HEAD_BYTES = 2048;         // one int4 per pair: the tile that starts there and ends in a later pair
     static constexpr int MAX_PAIRS = 128;                // the merge keeps four splits per lane
-    static constexpr int COMBINE_THREADS = 256;
+    static constexpr int COMBINE_THREADS = 256;         // at least MAX_PAIRS
 };
 static_assert(ChunkCfg::SMEM <= 232448, "shared memory exceeds the per-CTA limit");
 static_assert(ChunkCfg::OFF_P % 1024 == 0 && ChunkCfg::OFF_K % 1024 == 0 && ChunkCfg::OFF_V % 1024 == 0, "swizzled operands need 1024-byte alignment");
+static_assert(ChunkCfg::COMBINE_THREADS >= ChunkCfg::MAX_PAIRS, "one thread per header");
 static_assert(ChunkCfg::MAX_PAIRS * 16 <= ChunkCfg::HEAD_BYTES, "one header per pair");
 
 struct ChunkParams {
@@ -132,6 +133,14 @@ struct ChunkSeg {
     int32_t pad;
 };
 
+// One sequence as the list sees it.
+struct ChunkSeq {
+    int32_t row0, rows;       // its (token, head) rows
+    int32_t c, n, len;        // position of its first new token, new tokens, cached length
+    int32_t tiles, first;     // tiles; (c * H - 1) / 128, rounded down
+    int64_t blocks;           // blocks of all tiles
+};
+
 struct ChunkMisc {
     uint64_t k_full[ChunkCfg::KGROUPS];   // (CTA 0) the key group is ready in both CTAs
     uint64_t k_empty[ChunkCfg::KGROUPS];  // its MMAs have completed
@@ -147,6 +156,7 @@ struct ChunkMisc {
     ChunkSeg seg[ChunkCfg::NSEG];
     uint64_t wait_ns;
     int64_t start_before;               // blocks before the sequence that this pair starts in
+    ChunkSeq start_seq;
     int64_t sums[ChunkCfg::THREADS / 32];
     int32_t start_b;
     uint32_t tmem_base;
@@ -156,14 +166,6 @@ struct ChunkMisc {
 static_assert(sizeof(ChunkMisc) <= ChunkCfg::MISC_BYTES, "misc block exceeds its slot");
 
 // ------------------------------------------------------------------ the block list
-// One sequence as the list sees it.
-struct ChunkSeq {
-    int32_t row0, rows;       // its (token, head) rows
-    int32_t c, n, len;        // position of its first new token, new tokens, cached length
-    int32_t tiles, first;     // tiles; (c * H - 1) / 128, rounded down
-    int64_t blocks;           // blocks of all tiles
-};
-
 // sum over x < n of floor(x / h)
 __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t h) {
     const uint32_t q = n / h, r = n % h;
@@ -179,6 +181,15 @@ __device__ __forceinline__ int64_t tile_prefix(const ChunkSeq& s, int H, int i) 
     return (int64_t)i + floor_sum((uint32_t)(i + 1 + s.first), (uint32_t)H) - floor_sum((uint32_t)(1 + s.first), (uint32_t)H);
 }
 __device__ __forceinline__ int64_t last_tile_blocks(const ChunkSeq& s) { return (s.c + s.n - 1) / ChunkCfg::BLOCK + 1; }
+
+// pair_start and pair_of_block, without 64-bit divisions for lists of ordinary length.
+__device__ __forceinline__ int64_t share_start(int64_t total, int pr, int np) {
+    return total < (1 << 24) ? (int64_t)((uint32_t)total * (uint32_t)pr / (uint32_t)np) : pair_start(total, pr, np);
+}
+__device__ __forceinline__ int share_of(int64_t total, int64_t g, int np) {
+    return total < (1 << 24) ? (int)(((uint32_t)(g + 1) * (uint32_t)np + (uint32_t)total - 1) / (uint32_t)total) - 1
+                             : pair_of_block(total, g, np);
+}
 
 // Sequence b, with sizes that no input can push out of range: tokens past T are
 // dropped, a length is cut to the table's (both reported by `ok`).
@@ -338,28 +349,40 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     // ---------------------------------------------------------------- this pair's share of the list
     int64_t g0, g1, total;
     {
-        int64_t mine = 0, excl;
+        // the first THREADS sequences stay with their threads; more are counted, and looked for, in turns
+        int64_t excl;
         bool ok = true, all_ok = true;
-        for (int b = threadIdx.x; b < p.B; b += Cfg::THREADS) {
+        const ChunkSeq own = (int)threadIdx.x < p.B ? chunk_seq(p, (int)threadIdx.x, all_ok) : ChunkSeq{};
+        int64_t mine = 0;
+        for (int b = (int)threadIdx.x + Cfg::THREADS; b < p.B; b += Cfg::THREADS) {
             mine += chunk_seq(p, b, ok).blocks;
             all_ok = all_ok && ok;
         }
         if (!all_ok) atomicCAS(p.status, 0u, (uint32_t)kStBounds);
-        total = block_scan(mine, m->sums, excl);
+        const int64_t first = block_scan(own.blocks, m->sums, excl);
+        total = first;
+        if (p.B > Cfg::THREADS) {
+            int64_t unused;
+            total += block_scan(mine, m->sums, unused);
+        }
         // with fewer blocks than pairs, one each (the pairs behind them stay idle)
         np = (int)(total < np ? total : np);
-        g0 = pair < np ? pair_start(total, pair, np) : 0;
-        g1 = pair < np ? pair_start(total, pair + 1, np) : 0;
-        int64_t base = 0;
-        for (int b0 = 0; b0 < p.B && base <= g0 && g0 < g1; b0 += Cfg::THREADS) {
-            const int b = b0 + (int)threadIdx.x;
-            const int64_t v = b < p.B ? chunk_seq(p, b, ok).blocks : 0;
-            const int64_t sum = block_scan(v, m->sums, excl);
-            excl += base;
-            if (v > 0 && excl <= g0 && g0 < excl + v) {
+        g0 = pair < np ? share_start(total, pair, np) : 0;
+        g1 = pair < np ? share_start(total, pair + 1, np) : 0;
+        auto claim = [&](int b, const ChunkSeq& q, int64_t before) {
+            if (q.blocks > 0 && before <= g0 && g0 < before + q.blocks) {
                 m->start_b = b;
-                m->start_before = excl;
+                m->start_before = before;
+                m->start_seq = q;
             }
+        };
+        claim((int)threadIdx.x, own, excl);
+        int64_t base = first;
+        for (int b0 = Cfg::THREADS; b0 < p.B && base <= g0 && g0 < g1; b0 += Cfg::THREADS) {
+            const int b = b0 + (int)threadIdx.x;
+            const ChunkSeq q = b < p.B ? chunk_seq(p, b, ok) : ChunkSeq{};
+            const int64_t sum = block_scan(q.blocks, m->sums, excl);
+            claim(b, q, base + excl);
             base += sum;
         }
         __syncthreads();
@@ -375,7 +398,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         ChunkSeq s;
         bool sok;
         if (g0 < g1) {
-            s = chunk_seq(p, b, sok);
+            s = m->start_seq;
             const int64_t want = g0 - m->start_before;
             int lo = 0, hi = s.tiles;      // the tile is in [lo, hi)
             while (hi - lo > 1) {
@@ -430,7 +453,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 m->seg[r] = sg;
                 mbar_arrive(&m->seg_full[r]);
                 if (sg.part == 1)
-                    head = make_int4(sg.row0, sg.nrows, pair_of_block(total, tile_g0 + nb - 1, np) - pair + 1, 0);
+                    head = make_int4(sg.row0, sg.nrows, share_of(total, tile_g0 + nb - 1, np) - pair + 1, 0);
                 // Q, once every QK of the segment before has completed
                 if (ns > 0 && !mbar_spin(&m->q_empty, (ns - 1) & 1, abort, wlim)) {
                     ok = false;
@@ -543,7 +566,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             if (sg.b < 0) break;
             table = p.block_table + (int64_t)sg.b * p.max_blocks;
             const int k0 = __shfl_sync(0xffffffffu, sg.k0, 0), k1 = __shfl_sync(0xffffffffu, sg.k1, 0);
-            // page ids one block ahead, so that no load waits for one
+            // page ids one block ahead, so that no load waits for one.  (Asking for the pages in L2
+            // three blocks ahead made a decode step slower, 362 -> 432 us by lines, 477 by pages.)
             int a0 = page_id(2 * k0), a1 = page_id(2 * k0 + 1);
             for (int k = k0; ok && k < k1; ++k) {
                 const int b0 = page_id(2 * k + 2), b1 = page_id(2 * k + 3);
@@ -944,74 +968,110 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     if (threadIdx.x == 0 && m->abort) atomicCAS(p.status, 0u, (uint32_t)kStTimeout);
 }
 
-// Merge of the tiles whose blocks were spread over several pairs.  Block (x, y):
-// rows 8y.. of the tile that starts in pair x and ends in a later one (none: no
-// splits), one warp per row.  Split s of the tile is pair x + s's; with m_s its
-// running maximum (log2 units), l_s and e_s its sums of weights,
+// Merge of the tiles whose blocks were spread over several pairs.  Split s of the
+// tile that starts in pair x is pair x + s's; with m_s its running maximum (log2
+// units), l_s and e_s its sums of weights,
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,
 //   lse = (M + log2 sum_s 2^(m_s - M) e_s) ln 2,  M = max m_s,
-// added up in split order.
-__global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+// added up in split order.  The rows of all such tiles form one list (a scan over
+// the pairs' headers), shared out evenly; four warps take a row, 128 columns each,
+// with eight splits' loads in flight per lane (a tile of few rows may have as many
+// splits as there are pairs, and waiting for them one by one took 22 us).
+__global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kernel(const __grid_constant__ ChunkParams p,
+                                                                                  int np) {
     using Cfg = ChunkCfg;
+    constexpr int ROWS = Cfg::COMBINE_THREADS / 128;     // rows a block takes at a time
+    __shared__ int s_first[Cfg::MAX_PAIRS + 1];          // rows of the pairs before
+    __shared__ int4 s_head[Cfg::MAX_PAIRS];
+    __shared__ int s_sum[Cfg::COMBINE_THREADS / 32];
     griddep_wait();
-    const int pair = (int)blockIdx.x;
-    const int row = (int)blockIdx.y * (Cfg::COMBINE_THREADS / 32) + (int)(threadIdx.x >> 5);
-    const int lane = (int)(threadIdx.x & 31);
-    const int4 head = __ldcg(reinterpret_cast<const int4*>(p.part) + pair);
-    const int S = head.z;
-    if (row >= head.y || S < 2) return;
-    const int crank = row >> 6, hl = row & 63;
-    auto slot = [&](int s) -> const uint8_t* {
-        return p.part + Cfg::HEAD_BYTES + ((int64_t)(2 * (pair + s) + (s == 0 ? 1 : 0)) * 2 + crank) * Cfg::PART_BYTES;
-    };
+    const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+    int4 h = make_int4(0, 0, 0, 0);
+    if ((int)threadIdx.x < np) h = __ldcg(reinterpret_cast<const int4*>(p.part) + threadIdx.x);
+    const int mine = h.z >= 2 ? h.y : 0;
+    int x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    if ((int)threadIdx.x < Cfg::MAX_PAIRS) {
+        s_first[threadIdx.x + 1] = before + x;
+        s_head[threadIdx.x] = h;
+    }
+    if (threadIdx.x == 0) s_first[0] = 0;
+    __syncthreads();
+    const int rows = s_first[Cfg::MAX_PAIRS];
     constexpr int PER = Cfg::MAX_PAIRS / 32;
-    float w[PER], l = 0.0f, e = 0.0f, M = -INFINITY;
-    float4 st[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int s = lane + 32 * j;
-        st[j] = s < S ? __ldcg(reinterpret_cast<const float4*>(slot(s) + Cfg::PART_O) + hl)
-                      : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-        M = fmaxf(M, st[j].x);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        w[j] = st[j].x == -INFINITY ? 0.0f : exp2f(st[j].x - M);
-        l += w[j] * st[j].y;
-        e += w[j] * st[j].z;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        l += __shfl_xor_sync(0xffffffffu, l, d);
-        e += __shfl_xor_sync(0xffffffffu, e, d);
-    }
-    float4 acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-        for (int i = 0; i < 32 && 32 * j + i < S; ++i) {
-            const float ws = __shfl_sync(0xffffffffu, w[j], i);
-            if (ws == 0.0f) continue;
-            const float4* o = reinterpret_cast<const float4*>(slot(32 * j + i)) + hl * 128 + lane;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 v = __ldcg(o + 32 * q);
-                acc[q].x = fmaf(ws, v.x, acc[q].x);
-                acc[q].y = fmaf(ws, v.y, acc[q].y);
-                acc[q].z = fmaf(ws, v.z, acc[q].z);
-                acc[q].w = fmaf(ws, v.w, acc[q].w);
-            }
+    for (int i = (int)blockIdx.x * ROWS + warp / 4; i < rows; i += (int)gridDim.x * ROWS) {
+        int lo = 0, hi = Cfg::MAX_PAIRS - 1;             // the pair whose rows hold i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_first[mid] <= i) lo = mid;
+            else hi = mid - 1;
         }
-    const bool empty = l == 0.0f;
-    const float inv = empty ? 0.0f : 1.0f / l;
-    uint2* dst = reinterpret_cast<uint2*>(p.out + ((int64_t)head.x + row) * kDv) + lane;
+        const int row = i - s_first[lo], S = s_head[lo].z;
+        const int64_t out_row = (int64_t)s_head[lo].x + row;
+        const int crank = row >> 6, hl = row & 63;
+        auto slot = [&](int s) -> const uint8_t* {
+            return p.part + Cfg::HEAD_BYTES + ((int64_t)(2 * (lo + s) + (s == 0 ? 1 : 0)) * 2 + crank) * Cfg::PART_BYTES;
+        };
+        float w[PER], l = 0.0f, e = 0.0f, M = -INFINITY;
+        float4 st[PER];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        dst[32 * q] = make_uint2(pack_bf16(acc[q].x * inv, acc[q].y * inv), pack_bf16(acc[q].z * inv, acc[q].w * inv));
-    if (lane == 0 && p.lse) p.lse[(int64_t)head.x + row] = empty ? -INFINITY : (M + log2f(e)) * 0.69314718055994531f;
+        for (int j = 0; j < PER; ++j) {
+            const int s = lane + 32 * j;
+            st[j] = s < S ? __ldcg(reinterpret_cast<const float4*>(slot(s) + Cfg::PART_O) + hl)
+                          : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            M = fmaxf(M, st[j].x);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            w[j] = st[j].x == -INFINITY ? 0.0f : exp2f(st[j].x - M);
+            l += w[j] * st[j].y;
+            e += w[j] * st[j].z;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, d);
+            e += __shfl_xor_sync(0xffffffffu, e, d);
+        }
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int col = 128 * (warp & 3) + 4 * lane;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+#pragma unroll 1
+            for (int g = 0; g < 32 && 32 * j + g < S; g += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (32 * j + g + q < S)
+                        v[q] = __ldcg(reinterpret_cast<const float4*>(
+                            reinterpret_cast<const float*>(slot(32 * j + g + q)) + hl * 512 + col));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float ws = __shfl_sync(0xffffffffu, w[j], g + q);
+                    if (32 * j + g + q < S && ws != 0.0f) {
+                        acc.x = fmaf(ws, v[q].x, acc.x);
+                        acc.y = fmaf(ws, v[q].y, acc.y);
+                        acc.z = fmaf(ws, v[q].z, acc.z);
+                        acc.w = fmaf(ws, v[q].w, acc.w);
+                    }
+                }
+            }
+        const bool empty = l == 0.0f;
+        const float inv = empty ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint2*>(p.out + out_row * kDv + col) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if ((warp & 3) == 0 && lane == 0 && p.lse)
+            p.lse[out_row] = empty ? -INFINITY : (M + log2f(e)) * 0.69314718055994531f;
+    }
 }
 
 // ------------------------------------------------------------------ FP8 latent cache
