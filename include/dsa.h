@@ -411,11 +411,12 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  *     out[t,h,:] = sum_s softmax(S[t,h,:])_s row_s[0:512]
  *     lse[t,h] = log sum_s exp(S[t,h,s])
  * q, cache formats and block tables are those of sparse_mla_attn; an FP8 cache
- * is dequantized once per call into the scratch (bf16, rounded once), which
- * then holds max_seq_len rows for each sequence.
+ * is dequantized once per call into the scratch (fp16 with a power-of-two
+ * factor per page, rounded once: 2^-11 of a value), which then holds
+ * max_seq_len rows for each sequence.
  * out device [T, H, 512] bf16; lse device [T, H] fp32 (natural log) or NULL.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
- * bf16 for the second product.
+ * bf16 (fp16 over an FP8 cache) for the second product.
  * Rows of the cache at positions that a token does not see may hold anything,
  * and do not reach its result.  Rows of out and lse behind the last sequence
  * (t >= cu_q[B]) are left as they were.  Sequences without new tokens are

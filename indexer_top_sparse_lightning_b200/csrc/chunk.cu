@@ -15,11 +15,12 @@ using namespace dsa::host;
 
 namespace {
 
-// Scratch: [headers][partial slots of the pairs][FP8: the sequences' rows as bf16].
+// Scratch: [headers][partial slots of the pairs][FP8: the sequences' rows as fp16, and a
+// factor per page].
 struct ChunkPlan {
     int pairs = 0;
     int64_t pages = 0;          // FP8: pages per sequence of the copy
-    size_t copy_off = 0, total = 0;
+    size_t copy_off = 0, scale_off = 0, total = 0;
 };
 
 dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevInfo& di, ChunkPlan& pl) {
@@ -42,18 +43,19 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
     if (at->kv_dtype == DSA_KV_FP8) {
         pl.pages = ((int64_t)bt->max_seq_len + kPage - 1) / kPage;
         if (pl.pages * bt->batch > INT32_MAX / kPage) return DSA_ERR_UNSUPPORTED;   // rows of the copy, in 32 bits
-        pl.total += (size_t)pl.pages * bt->batch * kPage * kDqk * 2;
+        pl.scale_off = pl.copy_off + (size_t)pl.pages * bt->batch * kPage * kDqk * 2;
+        pl.total = align256(pl.scale_off + (size_t)pl.pages * bt->batch * 4);
     }
     return DSA_OK;
 }
 
 // Rows of 576 as [64 columns, rows, 9 chunks]: a box's 64-column chunks come out one
 // after another, each in the 128-byte rows that the MMA operands have.
-bool rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_chunks) {
+bool rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_chunks) {
     const uint64_t dims[3] = {64, rows, (uint64_t)ChunkCfg::KCH};
     const uint64_t strides[2] = {(uint64_t)kDqk * 2, 128};
     const uint32_t box[3] = {64, box_rows, box_chunks};
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return make_map(map, type, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -99,6 +101,8 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
         g.codes = static_cast<const uint8_t*>(at->kv_cache);
         g.scale = at->kv_scale;
         g.rows = reinterpret_cast<uint16_t*>(p.part + pl.copy_off);
+        g.page_scale = reinterpret_cast<float*>(p.part + pl.scale_off);
+        p.page_scale = g.page_scale;
         g.B = batch->batch;
         g.max_blocks = batch->max_blocks_per_seq;
         g.num_blocks = batch->num_blocks;
@@ -109,10 +113,12 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
         nrows = (uint64_t)pl.pages * batch->batch * kPage;
     }
     CUtensorMap tm_q, tm_k, tm_v;
-    if (!rows_map(&tm_q, at->q, (uint64_t)batch->num_tokens * at->H, 64, ChunkCfg::KCH) ||
-        !rows_map(&tm_k, rows, nrows, 64, 3) || !rows_map(&tm_v, rows, nrows, 32, 4))
+    const CUtensorMapDataType kt = pl.pages ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, 64, ChunkCfg::KCH) ||
+        !rows_map(&tm_k, kt, rows, nrows, 64, 3) || !rows_map(&tm_v, kt, rows, nrows, 32, 4))
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");
-    if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(&chunk_attn_kernel), ChunkCfg::SMEM))
+    const auto kernel = pl.pages ? &chunk_attn_kernel<true> : &chunk_attn_kernel<false>;
+    if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kernel), ChunkCfg::SMEM))
         return fail(DSA_ERR_CUDA, "shared memory attribute", e);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -129,7 +135,7 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaError_t e = cudaLaunchKernelEx(&cfg, &chunk_attn_kernel, p, tm_q, tm_k, tm_v))
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, tm_q, tm_k, tm_v))
         return fail(DSA_ERR_CUDA, "attention launch", e);
     if (pl.pairs < 2) return DSA_OK;
     cudaLaunchConfig_t ccfg;

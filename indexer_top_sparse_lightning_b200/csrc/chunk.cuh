@@ -86,14 +86,20 @@ struct ChunkCfg {
     static constexpr int SOFTMAX_WARPS = 8;
     static constexpr int QK_WARP = 8, PV_WARP = 9, KEY_WARP = 10, VALUE_WARP = 11, SEG_WARP = 12, FIX_WARP = 13;
     static constexpr int THREADS = 448;
-    // A row's reference maximum is replaced once a score exceeds it by 2^32: weights and sums
-    // are floating point, so a lower reference costs no precision, and 2^32 (2^52 for the sums of
-    // a million weights) is far from fp32's range.  A replacement waits for the P.V in flight.
-    static constexpr float LAZY = 32.0f;
+    // A row's reference (a maximum minus DROP) is replaced once a score exceeds it by more than LAZY.
+    // bf16 weights and fp32 sums are floating point, so a reference below the maximum costs no
+    // precision, and 2^32 (2^52 for the sums of a million weights) is far from fp32's range; a
+    // replacement waits for the P.V in flight.  fp16 weights end at 2^16 and lose bits below
+    // 2^-14: references seven below the maximum keep them in [2^-14, 2^15] down to 2^-21 of the
+    // largest weight, and to 2^-32 of it with an absolute error.
+    static constexpr float lazy(bool f16) { return f16 ? 15.0f : 32.0f; }
+    static constexpr float drop(bool f16) { return f16 ? 7.0f : 0.0f; }
     static constexpr int NSEG = 4;                      // segment ring
     static constexpr int TMEM_COLS = 512;               // O: [0, 256), two score buffers of 64 from column 256
-    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, BLOCK, false, false);
-    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, 256, false, true);
+    // fp16 operands: the bf16 descriptor without its two operand-format bits
+    static constexpr uint32_t BF16_BITS = (1u << 7) | (1u << 10);
+    static constexpr uint32_t idesc_qk(bool f16) { return idesc_bf16_f32(128, BLOCK, false, false) & ~(f16 ? BF16_BITS : 0u); }
+    static constexpr uint32_t idesc_pv(bool f16) { return idesc_bf16_f32(128, 256, false, true) & ~(f16 ? BF16_BITS : 0u); }
     // partial result of (pair, side, CTA): O [64 rows][512] fp32, then (m, sum, sum for lse, -) per row.
     // Side 1: the pair holds the tile's first blocks; side 0: later ones.
     static constexpr int64_t PART_O = 64 * 512 * 4;
@@ -116,7 +122,8 @@ struct ChunkParams {
     uint8_t* part;            // headers, then partial results
     uint32_t* status;         // status word; words 1-2 hold the test hooks
     int32_t B, T, H, max_blocks, num_blocks;
-    int32_t staged;           // > 0: the cache is a copy by sequence, `staged` pages each
+    int32_t staged;           // > 0: the cache is an fp16 copy by sequence, `staged` pages each
+    const float* page_scale;  // [B, staged] the copy's power-of-two factor of each page
     float scale_log2;         // sm_scale * log2(e)
 };
 
@@ -149,6 +156,7 @@ struct ChunkMisc {
     uint64_t v_peer[ChunkCfg::VRING];     // (CTA 0) CTA 1's fixer is done with the group
     uint64_t v_land[ChunkCfg::VRING];   // the group has landed, for the fixer to look at
     uint64_t q_full;                      // (CTA 0) Q of both CTAs
+    uint64_t q_land;                      // (fp16) this CTA's Q, still bf16
     uint64_t q_empty;
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t o_full, o_empty, drain[2];
@@ -236,6 +244,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
     return total;
 }
 
+// log2 of a power of two (a normal number).
+__device__ __forceinline__ float log2_of_power(float f) { return (float)((int)(__float_as_uint(f) >> 23) - 127); }
+
 // Waits of a whole warp: one lane polls (32 lanes' polls would each take a turn in
 // the shared-memory pipe that every other barrier operation needs), the rest
 // sleep at the warp's barrier.
@@ -269,6 +280,13 @@ __device__ __forceinline__ ChunkBlock chunk_block(const ChunkSeg& s, int k) {
     return r;
 }
 
+// F16: the cache is the fp16 copy of an FP8 cache (kv_fp8_pages_kernel), and Q is
+// brought to fp16 in shared memory: both operands of an MMA have one type, and
+// bf16 would round the products of codes and scales eight times as far.  Powers of two keep the values in fp16's range: one per row of Q,
+// one per page f_s of the copy.  With t_s = S_s + log2 f_s the weights that
+// multiply the copy's rows are P_s f_s = 2^(t_s - m), so the reference m follows
+// t, and the sums of weights are those of 2^(t_s - m) / f_s.
+template <bool F16>
 __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
@@ -299,7 +317,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             mbar_init(&m->v_empty[i], 1);
             mbar_init(&m->v_land[i], 1);
         }
-        mbar_init(&m->q_full, 2);
+        mbar_init(&m->q_full, F16 ? 2 * Cfg::SOFTMAX_WARPS : 2);
+        mbar_init(&m->q_land, 1);
         mbar_init(&m->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->s_full[i], 1);
@@ -459,8 +478,13 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx_cluster(q_full, Cfg::Q_BYTES);
-                tma_load_3d_pair(s_q, &tm_q, q_full, 0, sg.row0 + 64 * (int)crank, 0);
+                if constexpr (F16) {
+                    mbar_arrive_expect_tx(&m->q_land, Cfg::Q_BYTES);
+                    tma_load_3d(s_q, &tm_q, &m->q_land, 0, sg.row0 + 64 * (int)crank, 0);
+                } else {
+                    mbar_arrive_expect_tx_cluster(q_full, Cfg::Q_BYTES);
+                    tma_load_3d_pair(s_q, &tm_q, q_full, 0, sg.row0 + 64 * (int)crank, 0);
+                }
                 ++ns;
                 g = stop;
                 if (g < g1) {
@@ -637,6 +661,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     const int pos = k * Cfg::BLOCK + 32 * g + lane;
                     bool zero = pos >= sg.see;
                     if (!zero && pos >= sg.see_all) {
+                        constexpr uint32_t EXP = F16 ? 0x7C00u : 0x7F80u;
                         uint32_t odd = 0;  // an exponent of all ones
 #pragma unroll 1
                         for (int q = 0; q < 32; ++q) {
@@ -644,7 +669,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                odd |= (uint32_t)((w[e] & 0x7F80u) == 0x7F80u) | (uint32_t)((w[e] & 0x7F800000u) == 0x7F800000u);
+                                odd |= (uint32_t)((w[e] & EXP) == EXP) | (uint32_t)((w[e] & (EXP << 16)) == (EXP << 16));
                         }
                         zero = odd != 0;
                     }
@@ -695,7 +720,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     for (int j = 0; j < 12; ++j)
                         if (el) {
                             const uint32_t off = g * 1536 + (j >> 2) * 512 + (j & 3) * 2;
-                            umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::IDESC_QK, (g | j) != 0);
+                            umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::idesc_qk(F16), (g | j) != 0);
                         }
                     if (el) umma_commit_2cta(&m->k_empty[g], 3);
                 }
@@ -717,7 +742,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                         for (int s16 = 0; s16 < 2; ++s16)
                             if (el)        // A = P [64 rows x 16 positions] K-major
                                 umma_bf16_2cta(tm_o + h * 128, pd + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
-                                               vd + (h * 512 + s16 * 128), Cfg::IDESC_PV, g > 0 || s16 > 0 || !first);
+                                               vd + (h * 512 + s16 * 128), Cfg::idesc_pv(F16), g > 0 || s16 > 0 || !first);
                     if (el) umma_commit_2cta(&m->v_empty[r], 3);
                     if (++r == Cfg::VRING) {
                         r = 0;
@@ -803,12 +828,69 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 const int id = __ldg(table + page);
                 return id >= 0 && id < p.num_blocks;
             };
+            float c_row = p.scale_log2;                  // scores in log2 units
+            const float* page_scale = nullptr;
+            if constexpr (F16) {
+                page_scale = p.page_scale + (int64_t)sg.b * p.staged;
+                ok = warp_wait(&m->q_land, ns & 1, abort, wlim);
+                ok = named_bar_and(1, 256, ok);
+                if (!ok) break;
+                // This row's 72 pieces of 16 bytes, 18 for each of its threads (in an order that spreads
+                // the lanes over the banks): the largest magnitude, then fp16 of value * 2^(13 - E).
+                const int quarter = 2 * part + half;
+                auto piece = [&](int i) -> uint4* {
+                    const int j = 18 * quarter + i;
+                    return reinterpret_cast<uint4*>(s_q + (j >> 3) * 8192 + hl * 128 + (((j + hl) & 7) << 4));
+                };
+                uint32_t top = 0;                        // bf16 magnitudes compare as integers
+#pragma unroll 1
+                for (int i = 0; i < 18; ++i) {
+                    const uint4 v = *piece(i);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        top = max(top, w[e] & 0x7FFFu);
+                        top = max(top, (w[e] >> 16) & 0x7FFFu);
+                    }
+                }
+                float of[4];
+                exchange(__uint_as_float(top << 16), of);    // (NaN: above infinity as an integer)
+                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(of[e]) >> 16);
+                int E = (int)(top >> 7) - 127;
+                E = E < -100 ? -100 : E > 127 ? 127 : E;
+                const float down = __uint_as_float((uint32_t)(13 - E + 127) << 23);
+                c_row *= __uint_as_float((uint32_t)(E - 13 + 127) << 23);
+#pragma unroll 1
+                for (int i = 0; i < 18; ++i) {
+                    const uint4 v = *piece(i);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * down,
+                                                            __uint_as_float(w[e] & 0xFFFF0000u) * down);
+                        o[e] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    *piece(i) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&m->q_full, crank);
+            }
             bool next_ok = page_ok(sg.k0);
+            float next_f = 1.0f;
+            if constexpr (F16)
+                if ((2 * sg.k0 + half) * kPage < sg.see) next_f = __ldg(page_scale + 2 * sg.k0 + half);
             float mrun = -INFINITY, lrun = 0.0f, lfull = 0.0f;
             for (int k = sg.k0; k < sg.k1; ++k, ++blk) {
                 const uint32_t b = blk & 1, u = (blk >> 1) & 1;
                 const bool this_ok = next_ok;
-                if (k + 1 < sg.k1) next_ok = page_ok(k + 1);
+                const float fk = next_f;
+                if (k + 1 < sg.k1) {
+                    next_ok = page_ok(k + 1);
+                    if constexpr (F16)
+                        if ((2 * (k + 1) + half) * kPage < sg.see) next_f = __ldg(page_scale + 2 * (k + 1) + half);
+                }
                 const bool got = ok && warp_wait(&m->s_full[b], u, abort, wlim);
                 float sv[32];
                 float mx = -INFINITY;
@@ -823,25 +905,26 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     // positions of this thread that the row sees
                     const int vis = this_ok ? see - (k * Cfg::BLOCK + p0) : 0;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sv[i] = __uint_as_float(a[i]) * p.scale_log2;
+                    for (int i = 0; i < 32; ++i)
+                        sv[i] = F16 ? fmaf(__uint_as_float(a[i]), c_row * fk, log2_of_power(fk)) : __uint_as_float(a[i]) * c_row;
                     if (!__all_sync(0xffffffffu, vis >= 32))
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sv[i] = i < vis ? sv[i] : -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mx = fmaxf(mx, sv[i]);
                 }
-                // The reference maximum stays while no thread's scores are above it by more than LAZY
+                // The reference maximum stays while no thread's scores are above it by more than the limit
                 // (one barrier, no exchange); otherwise every row takes its new maximum.
                 float muse = mrun;
                 bool rescale = false;
-                if (!named_bar_and(1, 256, ok && got && !(mx > mrun + Cfg::LAZY))) {
+                if (!named_bar_and(1, 256, ok && got && !(mx > mrun + Cfg::lazy(F16)))) {
                     ok = named_bar_and(1, 256, ok && got);
                     if (!ok) break;
                     float of[4];
                     exchange(mx, of);
-                    const float mnew = fmaxf(mrun, fmaxf(fmaxf(of[0], of[1]), fmaxf(of[2], of[3])));
-                    rescale = mnew > mrun + Cfg::LAZY;      // identical in the four threads of a row
-                    if (rescale) muse = mnew;
+                    const float mnew = fmaxf(fmaxf(of[0], of[1]), fmaxf(of[2], of[3]));
+                    rescale = mnew > mrun + Cfg::lazy(F16);      // identical in the four threads of a row
+                    if (rescale) muse = mnew - Cfg::drop(F16);
                 }
                 const float base = muse == -INFINITY ? 0.0f : muse;   // (nothing seen yet: 2^-inf)
                 uint32_t pk[16];
@@ -850,11 +933,18 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 for (int i = 0; i < 16; ++i) {
                     const float e0 = fast_exp2(sv[2 * i] - base);
                     const float e1 = fast_exp2(sv[2 * i + 1] - base);
-                    pk[i] = pack_bf16(e0, e1);
-                    // O is divided by the sum of the bf16 weights that the MMA multiplies (their
-                    // roundings cancel in part); lse takes the sum before rounding
-                    r0 += __uint_as_float(pk[i] << 16);
-                    r1 += __uint_as_float(pk[i] & 0xFFFF0000u);
+                    // O is divided by the sum of the rounded weights that the MMA multiplies (their
+                    // roundings cancel in part); lse takes the sum before rounding.  fp16 weights
+                    // divide by that one as well: divided by a small page factor, the rounding of a
+                    // weight that is subnormal in fp16 would count in the sum as it does not in O.
+                    if constexpr (F16) {
+                        const __half2 h = __floats2half2_rn(e0, e1);
+                        pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        pk[i] = pack_bf16(e0, e1);
+                        r0 += __uint_as_float(pk[i] << 16);
+                        r1 += __uint_as_float(pk[i] & 0xFFFF0000u);
+                    }
                     f0 += e0;
                     f1 += e1;
                 }
@@ -881,8 +971,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                         tmem_wait_st();
                     }
                 }
-                lrun = lrun * f + (r0 + r1);
-                lfull = lfull * f + (f0 + f1);
+                lfull = fmaf(lfull, f, F16 ? (f0 + f1) / fk : f0 + f1);
+                lrun = F16 ? lfull : fmaf(lrun, f, r0 + r1);
                 mrun = muse;
                 if (ok) {
                     // P row hl, chunk of this half: four 16-byte pieces of a 128-byte row (128-byte swizzle)
@@ -1075,17 +1165,20 @@ __global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kerne
 }
 
 // ------------------------------------------------------------------ FP8 latent cache
-// The pages of every sequence, dequantized to bf16 (code x tile scale, rounded
-// once) into a copy that is laid out by sequence: page i of sequence b at
-// b * pages + i.  One block per page: its 64 rows are 2304 runs of 16 codes,
-// nine per thread, all loaded before any is converted.  Memory-bound: reads 596
-// bytes a row and writes 1152.
+// The pages of every sequence as fp16 (code x tile scale / page factor, rounded
+// once: 2^-11 of the value), in a copy that is laid out by sequence: page i of
+// sequence b at b * pages + i.  The page factor is the power of two that brings the
+// largest value that the page's scales allow below 2^14; positions behind the
+// sequence's end do not count, whatever they hold.  One block per page: its 64 rows
+// are 2304 runs of 16 codes, nine per thread, all loaded before any is converted.
+// Memory-bound: reads 596 bytes a row and writes 1152.
 struct PagesParams {
     const int32_t* seq_lens;
     const int32_t* block_table;
     const uint8_t* codes;       // [num_blocks * 64, 576]
     const float* scale;         // [num_blocks * 64, 5]
-    uint16_t* rows;             // [B * pages * 64, 576] bf16 bits
+    uint16_t* rows;             // [B * pages * 64, 576] fp16 bits
+    float* page_scale;          // [B * pages]
     int32_t B, max_blocks, num_blocks, pages;
 };
 
@@ -1093,27 +1186,54 @@ constexpr int kPagesThreads = 256;
 
 __global__ void __launch_bounds__(kPagesThreads) kv_fp8_pages_kernel(const __grid_constant__ PagesParams p) {
     griddep_launch_dependents();
+    __shared__ float s_top[kPagesThreads / 32];
     const int b = (int)blockIdx.x / p.pages, page = (int)blockIdx.x % p.pages;
-    if ((int64_t)page * kPage >= __ldg(p.seq_lens + b) || page >= p.max_blocks) return;
+    const int64_t left = (int64_t)__ldg(p.seq_lens + b) - (int64_t)page * kPage;
+    if (left <= 0 || page >= p.max_blocks) return;
     const int id = __ldg(p.block_table + (int64_t)b * p.max_blocks + page);
-    if (id < 0 || id >= p.num_blocks) return;          // the attention kernel reports it and does not read the copy
+    if (id < 0 || id >= p.num_blocks) {                // the attention kernel reports it and does not read the copy
+        if (threadIdx.x == 0) p.page_scale[blockIdx.x] = 1.0f;
+        return;
+    }
     constexpr int RUNS = kPage * kDqk / 16, PER = RUNS / kPagesThreads;
     static_assert(RUNS % kPagesThreads == 0, "whole runs per thread");
     const uint4* src = reinterpret_cast<const uint4*>(p.codes + (int64_t)id * kPage * kDqk);
     const float* sc = p.scale + (int64_t)id * kPage * kKvTiles;
-    uint4* dst = reinterpret_cast<uint4*>(p.rows + ((int64_t)b * p.pages + page) * kPage * kDqk);
+    uint4* dst = reinterpret_cast<uint4*>(p.rows + (int64_t)blockIdx.x * kPage * kDqk);
     uint4 v[PER];
-    float s[PER];
+    float s[PER], top = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int r = i * kPagesThreads + (int)threadIdx.x;
         v[i] = __ldg(src + r);
         s[i] = __ldg(sc + r / 36 * kKvTiles + r % 36 / 8);
+        if (r / 36 < left) top = fmaxf(top, fabsf(s[i]));
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPagesThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+    // scales below 2^(E + 1), codes up to 448 < 2^9: value / 2^(E - 4) < 2^14
+    int E = (int)(__float_as_uint(top) >> 23) - 127;
+    E = top == 0.0f ? 4 : E < -100 ? -100 : E > 120 ? 120 : E;
+    const float down = __uint_as_float((uint32_t)(4 - E + 127) << 23);
+    if (threadIdx.x == 0) p.page_scale[blockIdx.x] = __uint_as_float((uint32_t)(E - 4 + 127) << 23);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int r = i * kPagesThreads + (int)threadIdx.x;
-        stage_chunk(v[i], s[i], dst + 2 * r);
+        const float f = s[i] * down;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 x = e4m3x2_to_float2((uint16_t)(w[k / 2] >> (16 * (k & 1))));
+            const __half2 h = __floats2half2_rn(x.x * f, x.y * f);
+            o[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        dst[2 * r] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[2 * r + 1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 

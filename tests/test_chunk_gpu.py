@@ -11,6 +11,12 @@ D <= (576 + 8) 2^-23 * scale * sum_i |q_i k_i| (8: the scaling and the subtracti
 the running maximum), with 2^-21 for the exponential.  The value product adds
 (n + 8) 2^-23 of sum_s w_s |v_s|, the merge of partial results 130 more of 2^-24
 (both kept as (n + 140) 2^-23), and the output is rounded once (2^-8 of it).
+Over an FP8 cache the rows are rounded to fp16 (2^-11 of each value: that much of
+sum_i |q_i k_i| in D, and of sum_s w_s |v_s|), and the weights are fp16 and divided by
+their sum before rounding: 2^-11 of sum_s w_s |v_s|.  A product w f of a weight and its
+page's factor that is subnormal is off by 2^-32 of the largest such product (held near
+2^7), and meets v / f < 2^14, where f 2^14 is at most 2.3 times the page's largest
+value: 2.3 n 2^-32 of the largest weight times the largest value covers all n.
 lse: D + 2^-21, plus (n + 140) 2^-23 for the sum of n weights, plus 2^-22 of itself."""
 import math
 
@@ -26,9 +32,10 @@ pytestmark = pytest.mark.gpu
 SCALE = 1.0 / math.sqrt(ROW)
 
 
-def reference(pg, q, rows_of, scale=SCALE, hidden=None):
+def reference(pg, q, rows_of, scale=SCALE, hidden=None, fp16=False):
     """Per real token: (out, lse, bound of out's error, bound of lse's); 64 bits on the GPU.
-    rows_of(b): the latent rows of sequence b's positions; hidden(b): positions nobody sees."""
+    rows_of(b): the latent rows of sequence b's positions; hidden(b): positions nobody sees;
+    fp16: over an FP8 cache."""
     H = q.shape[1]
     res = [[], [], [], []]
     for b in range(pg.B):
@@ -53,11 +60,16 @@ def reference(pg, q, rows_of, scale=SCALE, hidden=None):
             w = (s - lse[..., None]).exp().nan_to_num(0.0)
             v = x[:, :DV]
             o = w @ v
-            D = (576 + 8) * 2.0 ** -23 * mag.amax(-1) + 2.0 ** -21
+            we, re = (2.0 ** -11, 2.0 ** -11) if fp16 else (2.0 ** -8, 0.0)
+            D = ((576 + 8) * 2.0 ** -23 + re) * mag.amax(-1) + 2.0 ** -21
             spread = torch.stack([(w[i, :, :, None] * (v[None] - o[i, :, None]).abs()).sum(1) for i in range(k)]) \
                 if k * H * L * DV < 2e8 else (w @ v.abs() + o.abs())      # >= sum w |v - o|
             acc = (L + 140) * 2.0 ** -23
-            bo = (2.0 ** -8 * (1 + 2.0 ** -7) + torch.expm1(2 * D)[..., None]) * spread + acc * (w @ v.abs())
+            if fp16:
+                bo = torch.expm1(2 * D)[..., None] * spread + (acc + re + we) * (w @ v.abs())
+                bo = bo + 2.3 * L * 2.0 ** -32 * w.amax(-1, keepdim=True) * v.abs().amax()
+            else:
+                bo = (we * (1 + 2 * we) + torch.expm1(2 * D)[..., None]) * spread + acc * (w @ v.abs())
             bo = bo + HALF_BF16 * (o.abs() + bo)
             bl = D + acc + 2.0 ** -22 * lse.abs()
             for r, y in zip(res, (o, lse, bo, bl)):
@@ -171,8 +183,25 @@ def test_fp8_latent_cache():
         used[pg.rows(b)] = True
     codes.view(-1, ROW)[~used] = 0x7F                  # NaN codes where nobody looks
     out, lse = run(pg, q, codes, kv_scale=scale.cuda())
-    bf = val.to(torch.bfloat16).double()               # the copy's one rounding
-    check(pg, out, lse, reference(pg, q, lambda b: bf.view(-1, ROW)[pg.rows(b)]))
+    check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
+
+
+def test_fp8_scales_of_any_size():
+    # pages whose scales lie far apart, queries far from 1: the powers of two that keep the fp16
+    # operands in range (a tile of zeros among them)
+    pg = Paged([700, 130], [3, 65], seed=12)
+    q = randn(31, pg.T, 20, ROW)
+    q[0] *= 2.0 ** -30
+    q[1] *= 2.0 ** 12
+    codes, scale, _ = fp8_rows(randn(32, pg.num_blocks, PAGE, ROW))
+    for b in range(2):
+        for i, page in enumerate(pg.table[b][pg.table[b] >= 0]):
+            scale[page] *= 2.0 ** ((-20, 3, 0, -7)[i % 4])
+    codes[pg.table[0][0], 3, 128:256] = 0
+    val = (codes.view(torch.float8_e4m3fn).double() *
+           scale.double().repeat_interleave(128, -1)[..., :ROW])
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
 
 
 def test_offsets_past_32_bits():
