@@ -411,9 +411,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  *     out[t,h,:] = sum_s softmax(S[t,h,:])_s row_s[0:512]
  *     lse[t,h] = log sum_s exp(S[t,h,s])
  * q, cache formats and block tables are those of sparse_mla_attn; an FP8 cache
- * is dequantized once per call into the scratch (fp16 with a power-of-two
- * factor per page, rounded once: 2^-11 of a value), which then holds
- * max_seq_len rows for each sequence.
+ * is dequantized once per call into the scratch (two fp16 values per element
+ * and a power-of-two factor per page; the scores take both, to 2^-22 of a value,
+ * the output the first, to 2^-11), which then holds max_seq_len rows of 2304
+ * bytes for each sequence.
  * out device [T, H, 512] bf16; lse device [T, H] fp32 (natural log) or NULL.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * bf16 (fp16 over an FP8 cache) for the second product.

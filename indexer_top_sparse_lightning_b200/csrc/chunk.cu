@@ -43,17 +43,18 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
     if (at->kv_dtype == DSA_KV_FP8) {
         pl.pages = ((int64_t)bt->max_seq_len + kPage - 1) / kPage;
         if (pl.pages * bt->batch > INT32_MAX / kPage) return DSA_ERR_UNSUPPORTED;   // rows of the copy, in 32 bits
-        pl.scale_off = pl.copy_off + (size_t)pl.pages * bt->batch * kPage * kDqk * 2;
+        pl.scale_off = pl.copy_off + (size_t)pl.pages * bt->batch * kPage * ChunkCfg::COPY_ROW * 2;
         pl.total = align256(pl.scale_off + (size_t)pl.pages * bt->batch * 4);
     }
     return DSA_OK;
 }
 
-// Rows of 576 as [64 columns, rows, 9 chunks]: a box's 64-column chunks come out one
+// Rows of `row` elements as [64 columns, rows, row / 64 chunks]: a box's 64-column chunks come out one
 // after another, each in the 128-byte rows that the MMA operands have.
-bool rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_chunks) {
-    const uint64_t dims[3] = {64, rows, (uint64_t)ChunkCfg::KCH};
-    const uint64_t strides[2] = {(uint64_t)kDqk * 2, 128};
+bool rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t row, uint32_t box_rows,
+              uint32_t box_chunks) {
+    const uint64_t dims[3] = {64, rows, row / 64};
+    const uint64_t strides[2] = {row * 2, 128};
     const uint32_t box[3] = {64, box_rows, box_chunks};
     return make_map(map, type, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
@@ -114,8 +115,9 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     }
     CUtensorMap tm_q, tm_k, tm_v;
     const CUtensorMapDataType kt = pl.pages ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, 64, ChunkCfg::KCH) ||
-        !rows_map(&tm_k, kt, rows, nrows, 64, 3) || !rows_map(&tm_v, kt, rows, nrows, 32, 4))
+    const uint64_t row = pl.pages ? ChunkCfg::COPY_ROW : kDqk;
+    if (!rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, kDqk, 64, ChunkCfg::KCH) ||
+        !rows_map(&tm_k, kt, rows, nrows, row, 64, 3) || !rows_map(&tm_v, kt, rows, nrows, row, 32, 4))
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");
     const auto kernel = pl.pages ? &chunk_attn_kernel<true> : &chunk_attn_kernel<false>;
     if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kernel), ChunkCfg::SMEM))

@@ -68,7 +68,9 @@ struct ChunkCfg {
     static constexpr int ROWS = 128;                    // (token, head) rows of a tile
     static constexpr int BLOCK = 128;                   // positions of a block (two pages)
     static constexpr int KCH = 9;                       // 64-column chunks of a latent row
-    static constexpr int KGROUPS = 3;                   // groups of a block's keys: 64 rows x 3 chunks
+    static constexpr int KRING = 3;                     // groups of keys (64 rows x 3 chunks) that are kept
+    static constexpr int kgroups(bool f16) { return f16 ? 6 : 3; }   // groups that make a block
+    static constexpr int COPY_ROW = 2 * kDqk;           // a row of the fp16 copy: values, then what rounding left
     static constexpr int KGROUP = 3 * 8192;
     static constexpr int VGROUPS = 4;                   // groups of a block's values: 32 rows x 4 chunks (this CTA's)
     static constexpr int VRING = 3;                     // groups that are kept
@@ -78,7 +80,7 @@ struct ChunkCfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
     static constexpr int OFF_K = OFF_P + 2 * P_BYTES;
-    static constexpr int OFF_V = OFF_K + KGROUPS * KGROUP;
+    static constexpr int OFF_V = OFF_K + KRING * KGROUP;
     static constexpr int OFF_XM = OFF_V + VRING * VGROUP;   // exchange between the threads of a row
     static constexpr int OFF_MISC = OFF_XM + 256 * 4;
     static constexpr int MISC_BYTES = 1024;
@@ -149,8 +151,8 @@ struct ChunkSeq {
 };
 
 struct ChunkMisc {
-    uint64_t k_full[ChunkCfg::KGROUPS];   // (CTA 0) the key group is ready in both CTAs
-    uint64_t k_empty[ChunkCfg::KGROUPS];  // its MMAs have completed
+    uint64_t k_full[ChunkCfg::KRING];   // (CTA 0) the key group is ready in both CTAs
+    uint64_t k_empty[ChunkCfg::KRING];  // its MMAs have completed
     uint64_t v_full[ChunkCfg::VRING];   // (CTA 0) the value group is ready in both CTAs
     uint64_t v_empty[ChunkCfg::VRING];
     uint64_t v_peer[ChunkCfg::VRING];     // (CTA 0) CTA 1's fixer is done with the group
@@ -282,7 +284,11 @@ __device__ __forceinline__ ChunkBlock chunk_block(const ChunkSeg& s, int k) {
 
 // F16: the cache is the fp16 copy of an FP8 cache (kv_fp8_pages_kernel), and Q is
 // brought to fp16 in shared memory: both operands of an MMA have one type, and
-// bf16 would round the products of codes and scales eight times as far.  Powers of two keep the values in fp16's range: one per row of Q,
+// bf16 would round the products of codes and scales eight times as far.  A row of
+// the copy holds the 576 rounded values and what their rounding left out; the
+// scores take both (twice the score MMAs and key loads: with the rounded values
+// alone lse was off by 6e-6 of itself, with both by 3e-7), the value product the
+// first.  Powers of two keep the values in fp16's range: one per row of Q,
 // one per page f_s of the copy.  With t_s = S_s + log2 f_s the weights that
 // multiply the copy's rows are P_s f_s = 2^(t_s - m), so the reference m follows
 // t, and the sums of weights are those of 2^(t_s - m) / f_s.
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     const int pair = (int)(blockIdx.x >> 1);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Cfg::KGROUPS; ++i) {
+        for (int i = 0; i < Cfg::KRING; ++i) {
             mbar_init(&m->k_full[i], 1);    // CTA 0's loader, for both CTAs
             mbar_init(&m->k_empty[i], 1);
         }
@@ -512,7 +518,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         // test hook: the second CTA never loads
         bool ok = !(crank == 1 && (m->inject & 4u));
         bool bad = false;
-        uint32_t r = 0, ph = 1;            // group of the ring and the parity that its `empty` waits for
+        uint32_t r = 0, ph = 1;            // group of the (value) ring and the parity that its `empty` waits for
         const uint32_t k_lead = mapa_shared(smem_u32(&m->k_full[0]), 0), v_lead = mapa_shared(smem_u32(&m->v_full[0]), 0);
         ChunkSeg sg = {};
         const int32_t* table = nullptr;
@@ -528,12 +534,13 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             const bool mine = el && id >= 0;
             const int y = id * kPage;
 #pragma unroll 1
-            for (int g = 0; g < Cfg::KGROUPS; ++g) {
-                if (!elected_wait(el, &m->k_empty[g], ph, abort, wlim)) return false;
-                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[g], bytes);
-                if (mine) tma_load_3d_pair(s_k + g * Cfg::KGROUP, &tm_k, k_lead + 8 * g, 0, y, 3 * g);
+            for (int g = 0; g < Cfg::kgroups(F16); ++g) {
+                const int kr = g % Cfg::KRING;
+                if (!elected_wait(el, &m->k_empty[kr], ph, abort, wlim)) return false;
+                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[kr], bytes);
+                if (mine) tma_load_3d_pair(s_k + kr * Cfg::KGROUP, &tm_k, k_lead + 8 * kr, 0, y, 3 * g);
+                if (kr == Cfg::KRING - 1) ph ^= 1;
             }
-            ph ^= 1;
             return true;
         };
         auto next_group = [&]() {
@@ -707,22 +714,25 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             // apart (LBO), 8-row groups 1024 B (SBO)
             const uint64_t v_desc = sdesc_sw128(smem_u32(s_v), 4096, 1024);
             uint32_t blk = 0;              // blocks so far
-            uint32_t r = 0, ph = 0;        // group of the value ring and its parity
+            uint32_t r = 0, ph = 0;        // group of the value ring; parity of the keys' or values' ring
             auto issue_qk = [&](bool last) -> bool {
                 // scores of this buffer's block before have been read
                 if (!elected_wait(el, &m->s_empty[blk & 1], ((blk >> 1) & 1) ^ 1, abort, wlim)) return false;
                 tc_fence_after();
                 const uint32_t d = tm_s + (blk & 1) * 64;
 #pragma unroll 1
-                for (int g = 0; g < Cfg::KGROUPS; ++g) {
-                    if (!elected_wait(el, &m->k_full[g], blk & 1, abort, wlim)) return false;
+                for (int g = 0; g < Cfg::kgroups(F16); ++g) {
+                    const int kr = g % Cfg::KRING;
+                    if (!elected_wait(el, &m->k_full[kr], ph, abort, wlim)) return false;
+                    const uint32_t base = kr * (Cfg::KGROUP / 16);   // of Q's chunks as well: 8192 bytes each
 #pragma unroll
                     for (int j = 0; j < 12; ++j)
                         if (el) {
-                            const uint32_t off = g * 1536 + (j >> 2) * 512 + (j & 3) * 2;
+                            const uint32_t off = base + (j >> 2) * 512 + (j & 3) * 2;
                             umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::idesc_qk(F16), (g | j) != 0);
                         }
-                    if (el) umma_commit_2cta(&m->k_empty[g], 3);
+                    if (el) umma_commit_2cta(&m->k_empty[kr], 3);
+                    if (kr == Cfg::KRING - 1) ph ^= 1;
                 }
                 if (el) umma_commit_2cta(&m->s_full[blk & 1], 3);
                 if (last && el) umma_commit_2cta(&m->q_empty, 3);
@@ -1165,19 +1175,19 @@ __global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kerne
 }
 
 // ------------------------------------------------------------------ FP8 latent cache
-// The pages of every sequence as fp16 (code x tile scale / page factor, rounded
-// once: 2^-11 of the value), in a copy that is laid out by sequence: page i of
+// The pages of every sequence as fp16: x = code x tile scale / page factor, rounded
+// (2^-11 of the value), and the rest x - that, rounded (2^-22), in a copy that is laid out by sequence: page i of
 // sequence b at b * pages + i.  The page factor is the power of two that brings the
 // largest value that the page's scales allow below 2^14; positions behind the
 // sequence's end do not count, whatever they hold.  One block per page: its 64 rows
 // are 2304 runs of 16 codes, nine per thread, all loaded before any is converted.
-// Memory-bound: reads 596 bytes a row and writes 1152.
+// Memory-bound: reads 596 bytes a row and writes 2304.
 struct PagesParams {
     const int32_t* seq_lens;
     const int32_t* block_table;
     const uint8_t* codes;       // [num_blocks * 64, 576]
     const float* scale;         // [num_blocks * 64, 5]
-    uint16_t* rows;             // [B * pages * 64, 576] fp16 bits
+    uint16_t* rows;             // [B * pages * 64, 2 x 576] fp16 bits
     float* page_scale;          // [B * pages]
     int32_t B, max_blocks, num_blocks, pages;
 };
@@ -1199,7 +1209,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_fp8_pages_kernel(const __gri
     static_assert(RUNS % kPagesThreads == 0, "whole runs per thread");
     const uint4* src = reinterpret_cast<const uint4*>(p.codes + (int64_t)id * kPage * kDqk);
     const float* sc = p.scale + (int64_t)id * kPage * kKvTiles;
-    uint4* dst = reinterpret_cast<uint4*>(p.rows + (int64_t)blockIdx.x * kPage * kDqk);
+    uint4* dst = reinterpret_cast<uint4*>(p.rows + (int64_t)blockIdx.x * kPage * ChunkCfg::COPY_ROW);
     uint4 v[PER];
     float s[PER], top = 0.0f;
 #pragma unroll
@@ -1225,15 +1235,21 @@ __global__ void __launch_bounds__(kPagesThreads) kv_fp8_pages_kernel(const __gri
         const int r = i * kPagesThreads + (int)threadIdx.x;
         const float f = s[i] * down;
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[8];
+        uint32_t o[8], rest[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float2 x = e4m3x2_to_float2((uint16_t)(w[k / 2] >> (16 * (k & 1))));
-            const __half2 h = __floats2half2_rn(x.x * f, x.y * f);
+            const float x0 = x.x * f, x1 = x.y * f;
+            const __half2 h = __floats2half2_rn(x0, x1);
+            const __half2 l = __floats2half2_rn(x0 - __low2float(h), x1 - __high2float(h));
             o[k] = *reinterpret_cast<const uint32_t*>(&h);
+            rest[k] = *reinterpret_cast<const uint32_t*>(&l);
         }
-        dst[2 * r] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[2 * r + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        uint4* d = dst + r / 36 * (ChunkCfg::COPY_ROW / 8) + 2 * (r % 36);
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        d[kDqk / 8] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+        d[kDqk / 8 + 1] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
     }
 }
 

@@ -11,8 +11,9 @@ D <= (576 + 8) 2^-23 * scale * sum_i |q_i k_i| (8: the scaling and the subtracti
 the running maximum), with 2^-21 for the exponential.  The value product adds
 (n + 8) 2^-23 of sum_s w_s |v_s|, the merge of partial results 130 more of 2^-24
 (both kept as (n + 140) 2^-23), and the output is rounded once (2^-8 of it).
-Over an FP8 cache the rows are rounded to fp16 (2^-11 of each value: that much of
-sum_i |q_i k_i| in D, and of sum_s w_s |v_s|), and the weights are fp16 and divided by
+Over an FP8 cache the rows are rounded to two fp16 values for the scores (2^-22 of each
+value: that much of sum_i |q_i k_i| in D, whose sum has twice the terms), to one for the
+output (2^-11 of sum_s w_s |v_s|), and the weights are fp16 and divided by
 their sum before rounding: 2^-11 of sum_s w_s |v_s|.  A product w f of a weight and its
 page's factor that is subnormal is off by 2^-32 of the largest such product (held near
 2^7), and meets v / f < 2^14, where f 2^14 is at most 2.3 times the page's largest
@@ -61,7 +62,7 @@ def reference(pg, q, rows_of, scale=SCALE, hidden=None, fp16=False):
             v = x[:, :DV]
             o = w @ v
             we, re = (2.0 ** -11, 2.0 ** -11) if fp16 else (2.0 ** -8, 0.0)
-            D = ((576 + 8) * 2.0 ** -23 + re) * mag.amax(-1) + 2.0 ** -21
+            D = ((1152 if fp16 else 576) + 8 + (2 if fp16 else 0)) * 2.0 ** -23 * mag.amax(-1) + 2.0 ** -21
             spread = torch.stack([(w[i, :, :, None] * (v[None] - o[i, :, None]).abs()).sum(1) for i in range(k)]) \
                 if k * H * L * DV < 2e8 else (w @ v.abs() + o.abs())      # >= sum w |v - o|
             acc = (L + 140) * 2.0 ** -23
