@@ -43,20 +43,10 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
     if (at->kv_dtype == DSA_KV_FP8) {
         pl.pages = ((int64_t)bt->max_seq_len + kPage - 1) / kPage;
         if (pl.pages * bt->batch > INT32_MAX / kPage) return DSA_ERR_UNSUPPORTED;   // rows of the copy, in 32 bits
-        pl.scale_off = pl.copy_off + (size_t)pl.pages * bt->batch * kPage * ChunkCfg::COPY_ROW * 2;
+        pl.scale_off = pl.copy_off + (size_t)pl.pages * bt->batch * kPage * kCopyRow * 2;
         pl.total = align256(pl.scale_off + (size_t)pl.pages * bt->batch * 4);
     }
     return DSA_OK;
-}
-
-// Rows of `row` elements as [64 columns, rows, row / 64 chunks]: a box's 64-column chunks come out one
-// after another, each in the 128-byte rows that the MMA operands have.
-bool rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t row, uint32_t box_rows,
-              uint32_t box_chunks) {
-    const uint64_t dims[3] = {64, rows, row / 64};
-    const uint64_t strides[2] = {row * 2, 128};
-    const uint32_t box[3] = {64, box_rows, box_chunks};
-    return make_map(map, type, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -91,31 +81,23 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     p.max_blocks = batch->max_blocks_per_seq;
     p.num_blocks = batch->num_blocks;
     p.staged = (int32_t)pl.pages;
+    const int64_t room = (pl.pages ? pl.pages : (int64_t)batch->max_blocks_per_seq) * kPage;
+    p.max_len = (int32_t)(room < INT32_MAX ? room : INT32_MAX);
+    p.tokens = p.max_tokens = INT32_MAX;
     p.scale_log2 = at->sm_scale * 1.4426950408889634f;
     const void* rows = at->kv_cache;
     uint64_t nrows = (uint64_t)batch->num_blocks * kPage;
     if (pl.pages) {
-        PagesParams g;
-        memset(&g, 0, sizeof g);
-        g.seq_lens = batch->seq_lens;
-        g.block_table = batch->block_table;
-        g.codes = static_cast<const uint8_t*>(at->kv_cache);
-        g.scale = at->kv_scale;
-        g.rows = reinterpret_cast<uint16_t*>(p.part + pl.copy_off);
-        g.page_scale = reinterpret_cast<float*>(p.part + pl.scale_off);
-        p.page_scale = g.page_scale;
-        g.B = batch->batch;
-        g.max_blocks = batch->max_blocks_per_seq;
-        g.num_blocks = batch->num_blocks;
-        g.pages = (int32_t)pl.pages;
-        kv_fp8_pages_kernel<<<(unsigned)(pl.pages * batch->batch), kPagesThreads, 0, s>>>(g);
-        if (cudaError_t e = cudaGetLastError()) return fail(DSA_ERR_CUDA, "latent copy launch", e);
-        rows = g.rows;
+        void* copy = p.part + pl.copy_off;
+        float* factors = reinterpret_cast<float*>(p.part + pl.scale_off);
+        if (dsa_status st = copy_fp8_pages(batch, at, pl.pages, copy, factors, s)) return st;
+        p.page_scale = factors;
+        rows = copy;
         nrows = (uint64_t)pl.pages * batch->batch * kPage;
     }
     CUtensorMap tm_q, tm_k, tm_v;
     const CUtensorMapDataType kt = pl.pages ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const uint64_t row = pl.pages ? ChunkCfg::COPY_ROW : kDqk;
+    const uint64_t row = pl.pages ? kCopyRow : kDqk;
     if (!rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, kDqk, 64, ChunkCfg::KCH) ||
         !rows_map(&tm_k, kt, rows, nrows, row, 64, 3) || !rows_map(&tm_v, kt, rows, nrows, row, 32, 4))
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");

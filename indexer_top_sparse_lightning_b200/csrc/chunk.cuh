@@ -13,8 +13,7 @@
 // contiguous share of it, so that the SMs finish together whatever the lengths.
 // A tile whose blocks are spread over several pairs leaves one partial result
 // per pair (unnormalized O, running maximum and sums, all fp32), merged by
-// chunk_combine_kernel.  The list is never stored: the blocks of a sequence's
-// first i tiles have a closed form (tile_prefix below).
+// chunk_combine_kernel.
 //
 // Per block the pair runs two-CTA tensor-core MMAs (tcgen05 cta_group::2,
 // issued by one thread of CTA 0):
@@ -58,9 +57,9 @@
 //   warp 13     fixer
 #pragma once
 #include "common.h"
-#include "fp8row.cuh"
 #include "pair.cuh"
 #include "ptx.cuh"
+#include "tiles.cuh"
 
 namespace dsa {
 
@@ -70,7 +69,6 @@ struct ChunkCfg {
     static constexpr int KCH = 9;                       // 64-column chunks of a latent row
     static constexpr int KRING = 3;                     // groups of keys (64 rows x 3 chunks) that are kept
     static constexpr int kgroups(bool f16) { return f16 ? 6 : 3; }   // groups that make a block
-    static constexpr int COPY_ROW = 2 * kDqk;           // a row of the fp16 copy: values, then what rounding left
     static constexpr int KGROUP = 3 * 8192;
     static constexpr int VGROUPS = 4;                   // groups of a block's values: 32 rows x 4 chunks (this CTA's)
     static constexpr int VRING = 3;                     // groups that are kept
@@ -115,39 +113,15 @@ static_assert(ChunkCfg::OFF_P % 1024 == 0 && ChunkCfg::OFF_K % 1024 == 0 && Chun
 static_assert(ChunkCfg::COMBINE_THREADS >= ChunkCfg::MAX_PAIRS, "one thread per header");
 static_assert(ChunkCfg::MAX_PAIRS * 16 <= ChunkCfg::HEAD_BYTES, "one header per pair");
 
-struct ChunkParams {
-    const int32_t* seq_lens;
-    const int32_t* cu_q;
-    const int32_t* block_table;
+using ChunkTiles = TileList<ChunkCfg::ROWS, ChunkCfg::BLOCK>;
+
+struct ChunkParams : ListParams {
     uint16_t* out;            // [T, H, 512] bf16 bits
     float* lse;               // [T, H] or null
     uint8_t* part;            // headers, then partial results
     uint32_t* status;         // status word; words 1-2 hold the test hooks
-    int32_t B, T, H, max_blocks, num_blocks;
-    int32_t staged;           // > 0: the cache is an fp16 copy by sequence, `staged` pages each
     const float* page_scale;  // [B, staged] the copy's power-of-two factor of each page
     float scale_log2;         // sm_scale * log2(e)
-};
-
-// A run of blocks of one tile.
-struct ChunkSeg {
-    int32_t b;                // sequence, -1: no more segments
-    int32_t row0;             // first (token, head) row of the tile, over the whole batch
-    int32_t nrows;            // rows of the tile (up to 128)
-    int32_t tok, head;        // token (in its sequence) and head of that row
-    int32_t c;                // position of the sequence's first new token
-    int32_t k0, k1;           // blocks
-    int32_t see_all, see;     // positions below see_all are seen by every row, none at or above see by any
-    int32_t part;             // 0: the whole tile; 1: its first blocks; 2: later blocks
-    int32_t pad;
-};
-
-// One sequence as the list sees it.
-struct ChunkSeq {
-    int32_t row0, rows;       // its (token, head) rows
-    int32_t c, n, len;        // position of its first new token, new tokens, cached length
-    int32_t tiles, first;     // tiles; (c * H - 1) / 128, rounded down
-    int64_t blocks;           // blocks of all tiles
 };
 
 struct ChunkMisc {
@@ -163,116 +137,22 @@ struct ChunkMisc {
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t o_full, o_empty, drain[2];
     uint64_t seg_full[ChunkCfg::NSEG], seg_empty[ChunkCfg::NSEG];
-    ChunkSeg seg[ChunkCfg::NSEG];
+    TileRun seg[ChunkCfg::NSEG];
     uint64_t wait_ns;
-    int64_t start_before;               // blocks before the sequence that this pair starts in
-    ChunkSeq start_seq;
+    ShareStart start;
     int64_t sums[ChunkCfg::THREADS / 32];
-    int32_t start_b;
     uint32_t tmem_base;
     int abort;
     uint32_t inject;
 };
 static_assert(sizeof(ChunkMisc) <= ChunkCfg::MISC_BYTES, "misc block exceeds its slot");
 
-// ------------------------------------------------------------------ the block list
-// sum over x < n of floor(x / h)
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t h) {
-    const uint32_t q = n / h, r = n % h;
-    return (int64_t)h * q * (q > 0 ? q - 1 : 0) / 2 + (int64_t)r * q;
-}
-
-// Blocks of the tiles before tile i (i < tiles).  Tile k < tiles - 1 ends with
-// row 128(k + 1) - 1, so it sees c + floor((128(k + 1) - 1) / H) + 1 positions,
-// in floor((c + floor((128(k + 1) - 1) / H)) / 128) + 1 blocks, which is
-// floor((k + 1 + first) / H) + 1 with first = floor((c H - 1) / 128) (nested
-// floors of quotients by integers commute).
-__device__ __forceinline__ int64_t tile_prefix(const ChunkSeq& s, int H, int i) {
-    return (int64_t)i + floor_sum((uint32_t)(i + 1 + s.first), (uint32_t)H) - floor_sum((uint32_t)(1 + s.first), (uint32_t)H);
-}
-__device__ __forceinline__ int64_t last_tile_blocks(const ChunkSeq& s) { return (s.c + s.n - 1) / ChunkCfg::BLOCK + 1; }
-
-// pair_start and pair_of_block, without 64-bit divisions for lists of ordinary length.
-__device__ __forceinline__ int64_t share_start(int64_t total, int pr, int np) {
-    return total < (1 << 24) ? (int64_t)((uint32_t)total * (uint32_t)pr / (uint32_t)np) : pair_start(total, pr, np);
-}
-__device__ __forceinline__ int share_of(int64_t total, int64_t g, int np) {
-    return total < (1 << 24) ? (int)(((uint32_t)(g + 1) * (uint32_t)np + (uint32_t)total - 1) / (uint32_t)total) - 1
-                             : pair_of_block(total, g, np);
-}
-
-// Sequence b, with sizes that no input can push out of range: tokens past T are
-// dropped, a length is cut to the table's (both reported by `ok`).
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool& ok) {
-    ChunkSeq s;
-    int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-    const int64_t cap = (int64_t)(p.staged ? p.staged : p.max_blocks) * kPage;
-    const int64_t len = __ldg(p.seq_lens + b);
-    ok = q0 >= 0 && q1 >= q0 && q1 <= p.T && len <= cap && (q1 == q0 || len >= q1 - q0);
-    q0 = q0 < 0 ? 0 : q0 > p.T ? p.T : q0;
-    q1 = q1 < q0 ? q0 : q1 > p.T ? p.T : q1;
-    s.n = q1 - q0;
-    s.len = (int)(len < 0 ? 0 : len > cap ? cap : len);
-    if (s.len < s.n) s.n = s.len;             // a sequence shorter than its new tokens: the rest sees nothing
-    s.c = s.len - s.n;
-    s.row0 = q0 * p.H;
-    s.rows = s.n * p.H;
-    s.tiles = (s.rows + ChunkCfg::ROWS - 1) / ChunkCfg::ROWS;
-    const int64_t ch = (int64_t)s.c * p.H;
-    s.first = ch > 0 ? (int)((ch - 1) / ChunkCfg::ROWS) : -1;
-    s.blocks = s.tiles > 0 ? tile_prefix(s, p.H, s.tiles - 1) + last_tile_blocks(s) : 0;
-    return s;
-}
-
-// Sum over the block's threads, the same in all of them; `excl` receives the sum
-// of the threads before this one.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& excl) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    int64_t total = 0, before = 0;
-    for (int w = 0; w < nw; ++w) {
-        if (w == warp) before = total;
-        total += sums[w];
-    }
-    excl = before + x - v;
-    return total;
-}
-
-// log2 of a power of two (a normal number).
-__device__ __forceinline__ float log2_of_power(float f) { return (float)((int)(__float_as_uint(f) >> 23) - 127); }
-
-// Waits of a whole warp: one lane polls (32 lanes' polls would each take a turn in
-// the shared-memory pipe that every other barrier operation needs), the rest
-// sleep at the warp's barrier.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_spin(bar, parity, abort, limit_ns);
-    __syncwarp();
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
-// The same in warps that act through an elected lane; the answer is uniform.
-__device__ __forceinline__ bool elected_wait(bool el, uint64_t* bar, uint32_t parity, volatile int* abort,
-                                             uint64_t limit_ns) {
-    bool ok = true;
-    if (el) ok = mbar_spin(bar, parity, abort, limit_ns);
-    return __all_sync(0xffffffffu, ok);
-}
-
 // The 32-position groups of a block that the value product runs over.
 struct ChunkBlock {
     int ngroups;              // 32-position groups that some row sees (1..4)
     int fix_from;             // first group that the fixer looks at (ngroups: none)
 };
-__device__ __forceinline__ ChunkBlock chunk_block(const ChunkSeg& s, int k) {
+__device__ __forceinline__ ChunkBlock chunk_block(const TileRun& s, int k) {
     ChunkBlock r;
     const int left = s.see - k * ChunkCfg::BLOCK;          // positions of the block that some row sees
     r.ngroups = left >= ChunkCfg::BLOCK ? 4 : left > 0 ? (left + 31) / 32 : 0;
@@ -282,7 +162,7 @@ __device__ __forceinline__ ChunkBlock chunk_block(const ChunkSeg& s, int k) {
     return r;
 }
 
-// F16: the cache is the fp16 copy of an FP8 cache (kv_fp8_pages_kernel), and Q is
+// F16: the cache is the fp16 copy of an FP8 cache (latent.cu), and Q is
 // brought to fp16 in shared memory: both operands of an MMA have one type, and
 // bf16 would round the products of codes and scales eight times as far.  A row of
 // the copy holds the 576 rounded values and what their rounding left out; the
@@ -340,7 +220,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             mbar_init(&m->seg_empty[i], Cfg::SOFTMAX_WARPS + (crank == 0 ? 5 : 3));   // loading and fixer warps; CTA 0: the issuers too
         }
         m->abort = 0;
-        m->start_b = -1;
+        m->start.b = -1;
         fence_mbar_init();
     }
     if (warp == Cfg::QK_WARP) {
@@ -373,71 +253,11 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
 
     // ---------------------------------------------------------------- this pair's share of the list
     int64_t g0, g1, total;
-    {
-        // the first THREADS sequences stay with their threads; more are counted, and looked for, in turns
-        int64_t excl;
-        bool ok = true, all_ok = true;
-        const ChunkSeq own = (int)threadIdx.x < p.B ? chunk_seq(p, (int)threadIdx.x, all_ok) : ChunkSeq{};
-        int64_t mine = 0;
-        for (int b = (int)threadIdx.x + Cfg::THREADS; b < p.B; b += Cfg::THREADS) {
-            mine += chunk_seq(p, b, ok).blocks;
-            all_ok = all_ok && ok;
-        }
-        if (!all_ok) atomicCAS(p.status, 0u, (uint32_t)kStBounds);
-        const int64_t first = block_scan(own.blocks, m->sums, excl);
-        total = first;
-        if (p.B > Cfg::THREADS) {
-            int64_t unused;
-            total += block_scan(mine, m->sums, unused);
-        }
-        // with fewer blocks than pairs, one each (the pairs behind them stay idle)
-        np = (int)(total < np ? total : np);
-        g0 = pair < np ? share_start(total, pair, np) : 0;
-        g1 = pair < np ? share_start(total, pair + 1, np) : 0;
-        auto claim = [&](int b, const ChunkSeq& q, int64_t before) {
-            if (q.blocks > 0 && before <= g0 && g0 < before + q.blocks) {
-                m->start_b = b;
-                m->start_before = before;
-                m->start_seq = q;
-            }
-        };
-        claim((int)threadIdx.x, own, excl);
-        int64_t base = first;
-        for (int b0 = Cfg::THREADS; b0 < p.B && base <= g0 && g0 < g1; b0 += Cfg::THREADS) {
-            const int b = b0 + (int)threadIdx.x;
-            const ChunkSeq q = b < p.B ? chunk_seq(p, b, ok) : ChunkSeq{};
-            const int64_t sum = block_scan(q.blocks, m->sums, excl);
-            claim(b, q, base + excl);
-            base += sum;
-        }
-        __syncthreads();
-    }
+    ChunkTiles::share<Cfg::THREADS>(p, pair, np, m->sums, &m->start, p.status, g0, g1, total);
 
     if (warp == Cfg::SEG_WARP) {
         // ---------------------------------------------------------------- segments, loads of Q
-        // The first tile by a search over 32 tiles at a time, the rest one by one.
-        int b = m->start_b;
-        int64_t g = g0;
-        int tile = 0;
-        int64_t tile_g0 = 0;               // the tile's first block in the list
-        ChunkSeq s;
-        bool sok;
-        if (g0 < g1) {
-            s = m->start_seq;
-            const int64_t want = g0 - m->start_before;
-            int lo = 0, hi = s.tiles;      // the tile is in [lo, hi)
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32;
-                const int i = lo + lane * step;
-                const bool at = i < hi && tile_prefix(s, p.H, i) <= want;   // true for a prefix of the lanes
-                const int nl = __popc(__ballot_sync(0xffffffffu, at));
-                const int nlo = lo + (nl - 1) * step;
-                hi = nlo + step < hi ? nlo + step : hi;
-                lo = nlo;
-            }
-            tile = lo;
-            tile_g0 = m->start_before + tile_prefix(s, p.H, tile);
-        }
+        ChunkTiles::Walk w = ChunkTiles::begin(p, m->start, g0, g1);
         // for the merge: first row, rows and pairs of the tile that starts here and ends in a later pair
         int4 head = make_int4(0, 0, 0, 0);
         bool ok = true;
@@ -450,35 +270,17 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     ok = false;
                     break;
                 }
-                ChunkSeg sg;
-                if (g >= g1) {
-                    sg.b = -1;
-                    m->seg[r] = sg;
+                if (w.g >= w.g1) {
+                    m->seg[r].b = -1;
                     mbar_arrive(&m->seg_full[r]);
                     break;
                 }
-                const int64_t nb = tile + 1 < s.tiles
-                                       ? (tile + 1 + s.first) / p.H + 1
-                                       : last_tile_blocks(s);
-                const int r0 = tile * Cfg::ROWS;
-                const int rows = s.rows - r0 < Cfg::ROWS ? s.rows - r0 : Cfg::ROWS;
-                const int64_t stop = tile_g0 + nb < g1 ? tile_g0 + nb : g1;
-                sg.b = b;
-                sg.row0 = s.row0 + r0;
-                sg.nrows = rows;
-                sg.tok = r0 / p.H;
-                sg.head = r0 % p.H;
-                sg.c = s.c;
-                sg.k0 = (int)(g - tile_g0);
-                sg.k1 = (int)(stop - tile_g0);
-                sg.see_all = s.c + sg.tok + 1;
-                sg.see = s.c + (r0 + rows - 1) / p.H + 1;
-                sg.part = sg.k0 == 0 && stop == tile_g0 + nb ? 0 : sg.k0 == 0 ? 1 : 2;
-                sg.pad = 0;
+                int64_t nb;
+                const TileRun sg = ChunkTiles::run(p, w, nb);
                 m->seg[r] = sg;
                 mbar_arrive(&m->seg_full[r]);
                 if (sg.part == 1)
-                    head = make_int4(sg.row0, sg.nrows, share_of(total, tile_g0 + nb - 1, np) - pair + 1, 0);
+                    head = make_int4(sg.row0, sg.nrows, share_of(total, w.tile_g0 + nb - 1, np) - pair + 1, 0);
                 // Q, once every QK of the segment before has completed
                 if (ns > 0 && !mbar_spin(&m->q_empty, (ns - 1) & 1, abort, wlim)) {
                     ok = false;
@@ -492,16 +294,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     tma_load_3d_pair(s_q, &tm_q, q_full, 0, sg.row0 + 64 * (int)crank, 0);
                 }
                 ++ns;
-                g = stop;
-                if (g < g1) {
-                    // the next tile, of this sequence or of a later one
-                    if (++tile == s.tiles) {
-                        tile = 0;
-                        do s = chunk_seq(p, ++b, sok);
-                        while (s.blocks == 0 && b + 1 < p.B);
-                    }
-                    tile_g0 = g;
-                }
+                ChunkTiles::next(p, w, sg);
             }
             if (!ok) *abort = 1;
             if (crank == 0) reinterpret_cast<int4*>(p.part)[pair] = head;
@@ -520,7 +313,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         bool bad = false;
         uint32_t r = 0, ph = 1;            // group of the (value) ring and the parity that its `empty` waits for
         const uint32_t k_lead = mapa_shared(smem_u32(&m->k_full[0]), 0), v_lead = mapa_shared(smem_u32(&m->v_full[0]), 0);
-        ChunkSeg sg = {};
+        TileRun sg = {};
         const int32_t* table = nullptr;
         auto page_id = [&](int page) -> int {          // -1: nobody sees the page; -2: a bad id
             if (page >= p.max_blocks || page * kPage >= sg.see) return -1;
@@ -626,7 +419,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 ok = false;
                 break;
             }
-            const ChunkSeg sg = m->seg[sr];
+            const TileRun sg = m->seg[sr];
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->seg_empty[sr]);
             if (sg.b < 0) break;
@@ -769,7 +562,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     ok = false;
                     break;
                 }
-                const ChunkSeg sg = m->seg[sr];
+                const TileRun sg = m->seg[sr];
                 __syncwarp();
                 if (el) mbar_arrive(&m->seg_empty[sr]);
                 if (sg.b < 0) break;
@@ -822,7 +615,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             const bool there = warp_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim);
             ok = named_bar_and(1, 256, ok && there);
             if (!ok) break;
-            const ChunkSeg sg = m->seg[sr];
+            const TileRun sg = m->seg[sr];
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->seg_empty[sr]);
             if (sg.b < 0) break;
@@ -1171,85 +964,6 @@ __global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kerne
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
         if ((warp & 3) == 0 && lane == 0 && p.lse)
             p.lse[out_row] = empty ? -INFINITY : (M + log2f(e)) * 0.69314718055994531f;
-    }
-}
-
-// ------------------------------------------------------------------ FP8 latent cache
-// The pages of every sequence as fp16: x = code x tile scale / page factor, rounded
-// (2^-11 of the value), and the rest x - that, rounded (2^-22), in a copy that is laid out by sequence: page i of
-// sequence b at b * pages + i.  The page factor is the power of two that brings the
-// largest value that the page's scales allow below 2^14; positions behind the
-// sequence's end do not count, whatever they hold.  One block per page: its 64 rows
-// are 2304 runs of 16 codes, nine per thread, all loaded before any is converted.
-// Memory-bound: reads 596 bytes a row and writes 2304.
-struct PagesParams {
-    const int32_t* seq_lens;
-    const int32_t* block_table;
-    const uint8_t* codes;       // [num_blocks * 64, 576]
-    const float* scale;         // [num_blocks * 64, 5]
-    uint16_t* rows;             // [B * pages * 64, 2 x 576] fp16 bits
-    float* page_scale;          // [B * pages]
-    int32_t B, max_blocks, num_blocks, pages;
-};
-
-constexpr int kPagesThreads = 256;
-
-__global__ void __launch_bounds__(kPagesThreads) kv_fp8_pages_kernel(const __grid_constant__ PagesParams p) {
-    griddep_launch_dependents();
-    __shared__ float s_top[kPagesThreads / 32];
-    const int b = (int)blockIdx.x / p.pages, page = (int)blockIdx.x % p.pages;
-    const int64_t left = (int64_t)__ldg(p.seq_lens + b) - (int64_t)page * kPage;
-    if (left <= 0 || page >= p.max_blocks) return;
-    const int id = __ldg(p.block_table + (int64_t)b * p.max_blocks + page);
-    if (id < 0 || id >= p.num_blocks) {                // the attention kernel reports it and does not read the copy
-        if (threadIdx.x == 0) p.page_scale[blockIdx.x] = 1.0f;
-        return;
-    }
-    constexpr int RUNS = kPage * kDqk / 16, PER = RUNS / kPagesThreads;
-    static_assert(RUNS % kPagesThreads == 0, "whole runs per thread");
-    const uint4* src = reinterpret_cast<const uint4*>(p.codes + (int64_t)id * kPage * kDqk);
-    const float* sc = p.scale + (int64_t)id * kPage * kKvTiles;
-    uint4* dst = reinterpret_cast<uint4*>(p.rows + (int64_t)blockIdx.x * kPage * ChunkCfg::COPY_ROW);
-    uint4 v[PER];
-    float s[PER], top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int r = i * kPagesThreads + (int)threadIdx.x;
-        v[i] = __ldg(src + r);
-        s[i] = __ldg(sc + r / 36 * kKvTiles + r % 36 / 8);
-        if (r / 36 < left) top = fmaxf(top, fabsf(s[i]));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kPagesThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-    // scales below 2^(E + 1), codes up to 448 < 2^9: value / 2^(E - 4) < 2^14
-    int E = (int)(__float_as_uint(top) >> 23) - 127;
-    E = top == 0.0f ? 4 : E < -100 ? -100 : E > 120 ? 120 : E;
-    const float down = __uint_as_float((uint32_t)(4 - E + 127) << 23);
-    if (threadIdx.x == 0) p.page_scale[blockIdx.x] = __uint_as_float((uint32_t)(E - 4 + 127) << 23);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int r = i * kPagesThreads + (int)threadIdx.x;
-        const float f = s[i] * down;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[8], rest[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 x = e4m3x2_to_float2((uint16_t)(w[k / 2] >> (16 * (k & 1))));
-            const float x0 = x.x * f, x1 = x.y * f;
-            const __half2 h = __floats2half2_rn(x0, x1);
-            const __half2 l = __floats2half2_rn(x0 - __low2float(h), x1 - __high2float(h));
-            o[k] = *reinterpret_cast<const uint32_t*>(&h);
-            rest[k] = *reinterpret_cast<const uint32_t*>(&l);
-        }
-        uint4* d = dst + r / 36 * (ChunkCfg::COPY_ROW / 8) + 2 * (r % 36);
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        d[kDqk / 8] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-        d[kDqk / 8 + 1] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
     }
 }
 

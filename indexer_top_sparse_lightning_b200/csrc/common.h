@@ -11,6 +11,7 @@ constexpr int kTileKeys = 128;        // keys per indexer MMA tile (two pages)
 constexpr int kMaxTopK = 2048;
 constexpr int kDqk = 576;             // latent 512 + RoPE 64
 constexpr int kDv = 512;
+constexpr int kCopyRow = 2 * kDqk;    // a row of the fp16 copy of an FP8 cache: values, then what rounding left
 constexpr int kEpiWarps = 8;          // indexer epilogue / Top-K warps (two per TMEM lane quarter)
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kConvThreads = 192;     // fp8 key widening threads (six warps)

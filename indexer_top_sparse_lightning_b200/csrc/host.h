@@ -27,6 +27,18 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* ba
               const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz,
               CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
+// Rows of `row` 16-bit elements as [64 columns, rows, row / 64 chunks]: a box's 64-column
+// chunks come out one after another, each in the 128-byte rows that MMA operands have.
+bool rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t row, uint32_t box_rows,
+              uint32_t box_chunks);
+
+// The fp16 copy of an FP8 latent cache, by sequence (`pages` pages each: rows of kCopyRow
+// values, and a power-of-two factor per page), and that of bf16 queries (rows of 576, and a
+// power-of-two factor per row).
+dsa_status copy_fp8_pages(const dsa_batch* bt, const dsa_attn_inputs* at, int64_t pages, void* rows, float* page_scale,
+                          cudaStream_t stream);
+dsa_status copy_fp16_queries(const void* q, int64_t nrows, void* out, float* factor, cudaStream_t stream);
+
 // cudaFuncSetAttribute for the dynamic shared memory of `fn`, once per
 // (kernel, device, size).
 cudaError_t set_smem_attr(const void* fn, int bytes);
