@@ -436,6 +436,34 @@ DSA_API size_t dsa_chunk_scratch_size(const dsa_batch* batch, const dsa_attn_inp
 DSA_API dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, void* out, float* lse,
                                   void* status, void* scratch, size_t scratch_bytes, void* stream);
 
+/*
+ * Attention weight of the cached positions: how much of their softmax weight the
+ * step's new tokens gave to each position, summed over tokens and heads and added
+ * to what the position had,
+ *     weight[b, s] = decay * weight[b, s]
+ *                    + sum_{j, h} exp(sm_scale * q[t,h,:] . row_s[0:576] - lse[t,h])
+ * over the new tokens j of sequence b that see s (s <= p_t), for every
+ * s < seq_lens[b].  lse [T, H] is what dsa_chunk_attn or sparse_mla_attn returned
+ * for these queries (after sparse attention the weights of positions outside the
+ * selection come out as if they had been attended to under the same lse); a row
+ * whose lse is -inf adds nothing.  The sums accumulate what dsa_cache_evict
+ * chooses by.
+ * weight device [B, stride] fp32, stride >= max_seq_len elements; entries at
+ * s >= seq_lens[b], and all of a sequence without new tokens, are left as they
+ * were.  decay >= 0, finite; with 0 the old weights are not read.
+ * q, cache formats, block tables, status and the bounds reported there are those
+ * of dsa_chunk_attn; positions of a page whose id is out of range add nothing.
+ * More than max_q_per_seq new tokens of a sequence, or a length above max_seq_len,
+ * are recorded as DSA_ERR_DEVICE_BOUNDS (the surplus is not counted).
+ * scratch: dsa_weight_scratch_size bytes, 256-byte aligned, of any contents, one
+ * each for calls that may overlap in time.  The sums are added in a fixed order:
+ * equal calls give equal bits.  Errors as for dsa_chunk_attn.
+ */
+DSA_API size_t dsa_weight_scratch_size(const dsa_batch* batch, const dsa_attn_inputs* at);
+DSA_API dsa_status dsa_attn_weight(const dsa_batch* batch, const dsa_attn_inputs* at, const float* lse, float* weight,
+                                   int64_t stride, float decay, void* status, void* scratch, size_t scratch_bytes,
+                                   void* stream);
+
 /* Static description of a status code. */
 DSA_API const char* dsa_status_str(int32_t status);
 

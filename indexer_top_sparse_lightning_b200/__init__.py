@@ -20,6 +20,8 @@ Entry points (same names as the C ABI):
         (per-head norm and rotation of queries and keys; keys go into the paged cache)
     dsa_chunk_attn(batch, q, kv_cache, sm_scale, kv_scale=None) -> (out, lse)
         (dense causal attention of the new tokens over the paged latent cache)
+    dsa_attn_weight(batch, q, kv_cache, sm_scale, lse, weight, decay=1.0, kv_scale=None) -> weight
+        (the attention weight that each cached position draws, accumulated)
 
 Key formats: bf16 keys (k_scale None); e4m3 keys (uint8) with fp32 k_scale
 [nblk, 64, D_I/64]; MXFP8 queries and keys when q_scale is given: q_idx and
@@ -36,7 +38,7 @@ from typing import Optional
 import torch
 
 __all__ = ["Batch", "Workspace", "indexer_topk", "sparse_mla_attn", "dsa_decode", "indexer_prolog",
-           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "dsa_chunk_attn", "get_status", "status_workspace",
+           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "dsa_chunk_attn", "dsa_attn_weight", "get_status", "status_workspace",
            "DsaError", "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -151,6 +153,11 @@ def load_library():
     lib.dsa_chunk_attn.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_chunk_attn.restype = ctypes.c_int
+    lib.dsa_weight_scratch_size.argtypes = [P(_Batch), P(_Attn)]
+    lib.dsa_weight_scratch_size.restype = ctypes.c_size_t
+    lib.dsa_attn_weight.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.dsa_attn_weight.restype = ctypes.c_int
     lib.dsa_status_str.argtypes = [ctypes.c_int32]
     lib.dsa_status_str.restype = ctypes.c_char_p
     lib.dsa_version.restype = ctypes.c_char_p
@@ -492,7 +499,7 @@ _status_ws = {}
 
 
 def status_workspace(device=None) -> Workspace:
-    """The default status area of dsa_qk_norm_rope and dsa_chunk_attn on a
+    """The default status area of the dsa_ operators over the paged cache on a
     device: read it with get_status(status_workspace(device)).  It keeps its address for
     the life of the process, so captured graphs may hold it."""
     key = None if device is None else torch.device(device).index
@@ -681,6 +688,29 @@ def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None,
     if rc != 0:
         raise DsaError(rc, "dsa_chunk_attn")
     return out, lse
+
+
+def dsa_attn_weight(batch: Batch, q, kv_cache, sm_scale: float, lse, weight, *, decay: float = 1.0, kv_scale=None,
+                    workspace: Optional[Workspace] = None, stream=None):
+    """Adds to weight [B, >= max_seq_len] fp32 (after scaling what it holds by decay) the softmax
+    weight that the step's new tokens give to each cached position, over tokens and heads; lse
+    [T, H] is the attention's.  Returns weight."""
+    lib = load_library()
+    at, T, H, dev = _latent_attn(q, kv_cache, sm_scale, kv_scale, batch.num_blocks)
+    cb = _batch_struct(batch, T, dev)
+    lp = _dense(lse, "lse", torch.float32, (T, H), dev)
+    n = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 2 else None
+    wp = _dense(weight, "weight", torch.float32, (cb.batch, n), dev)
+    status = _ptr((workspace if workspace is not None else status_workspace(q.device)).get(256))
+    with _On(dev, stream) as on:
+        need = lib.dsa_weight_scratch_size(ctypes.byref(cb), ctypes.byref(at))
+        if need == 0:
+            raise DsaError(2, "dsa_weight_scratch_size")
+        scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
+        rc = lib.dsa_attn_weight(ctypes.byref(cb), ctypes.byref(at), lp, wp, n, decay, status, scratch.data_ptr(), need, on)
+    if rc != 0:
+        raise DsaError(rc, "dsa_attn_weight")
+    return weight
 
 
 def decode_launch_count(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm_scale: float,
