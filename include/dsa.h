@@ -464,6 +464,50 @@ DSA_API dsa_status dsa_attn_weight(const dsa_batch* batch, const dsa_attn_inputs
                                    int64_t stride, float decay, void* status, void* scratch, size_t scratch_bytes,
                                    void* stream);
 
+/*
+ * Eviction from the paged caches: of each sequence's L = seq_lens[b] positions,
+ * `keep` stay (all, when L <= keep): the first `sink`, the last `recent`, and of
+ * the others those with the largest weight (dsa_attn_weight's; ties and equal
+ * weights: the lower position stays; -0 equals 0; NaN goes first).
+ * out_idx device [B, keep] receives the positions that stay, ascending, -1 padded;
+ * out_len device [B] how many.  The rows of every array are copied, in that
+ * order, to the sequence's new pages: position out_idx[b, j] becomes position j,
+ * in page new_table[b, j / 64].  new_weight, if given, receives their weights in
+ * the same order (entries behind out_len[b] are left as they were).  Rows keep the
+ * rotation they were written with, so the tokens that follow are given their
+ * rotation positions explicitly (dsa_rope_inputs.positions): the cached length is
+ * no longer their place in the text.
+ * The arrays may be the caches themselves (dst = src) when no new page is a page
+ * that any sequence of the batch still reads from here; new pages must be
+ * distinct.  batch->cu_q and max_q_per_seq are not used (but checked).
+ * A page id out of range is recorded as DSA_ERR_DEVICE_BOUNDS and the row is not
+ * copied; a length above max_seq_len likewise, and is taken as max_seq_len.
+ */
+typedef struct {
+    const void* src;            /* device [num_blocks, 64, row_bytes]                                  */
+    void* dst;                  /* device [new_num_blocks, 64, row_bytes]                              */
+    int64_t row_bytes;          /* bytes per position; wider copies when rows are 16-byte aligned      */
+} dsa_cache_array;
+
+typedef struct {
+    const float* weight;        /* device [B, weight_stride], weight_stride >= max_seq_len             */
+    int64_t weight_stride;
+    float* new_weight;          /* device [B, new_weight_stride] or NULL; not weight itself            */
+    int64_t new_weight_stride;  /* >= min(keep, max_seq_len)                                           */
+    int32_t keep;               /* positions that stay, >= 1                                           */
+    int32_t sink;               /* first positions that stay in any case, >= 0                         */
+    int32_t recent;             /* last positions that stay in any case; sink + recent <= keep         */
+    const int32_t* new_table;   /* device [B, new_max_blocks]                                          */
+    int32_t new_max_blocks;     /* room for min(keep, max_seq_len) positions                           */
+    int32_t new_num_blocks;     /* physical pages in each dst (bounds checks)                          */
+    const dsa_cache_array* arrays; /* HOST array of n_arrays (read during the call), or NULL           */
+    int32_t n_arrays;           /* 0..8                                                                */
+} dsa_evict_inputs;
+
+/* Two launches (one when there is nothing to copy); status as for dsa_chunk_attn, errors too. */
+DSA_API dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, int32_t* out_idx, int32_t* out_len,
+                                   void* status, void* stream);
+
 /* Static description of a status code. */
 DSA_API const char* dsa_status_str(int32_t status);
 

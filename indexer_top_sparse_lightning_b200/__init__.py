@@ -22,6 +22,8 @@ Entry points (same names as the C ABI):
         (dense causal attention of the new tokens over the paged latent cache)
     dsa_attn_weight(batch, q, kv_cache, sm_scale, lse, weight, decay=1.0, kv_scale=None) -> weight
         (the attention weight that each cached position draws, accumulated)
+    dsa_cache_evict(batch, weight, keep, new_table, arrays, new_arrays, sink=0, recent=0, new_weight=None) -> (idx, len)
+        (keeps the positions with the most weight; their rows move to new pages)
 
 Key formats: bf16 keys (k_scale None); e4m3 keys (uint8) with fp32 k_scale
 [nblk, 64, D_I/64]; MXFP8 queries and keys when q_scale is given: q_idx and
@@ -38,7 +40,7 @@ from typing import Optional
 import torch
 
 __all__ = ["Batch", "Workspace", "indexer_topk", "sparse_mla_attn", "dsa_decode", "indexer_prolog",
-           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "dsa_chunk_attn", "dsa_attn_weight", "get_status", "status_workspace",
+           "prolog_pack_weights", "PackedWeights", "dsa_qk_norm_rope", "dsa_chunk_attn", "dsa_attn_weight", "dsa_cache_evict", "get_status", "status_workspace",
            "DsaError", "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -101,6 +103,18 @@ class _Rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p), ("kv_dtype", ctypes.c_int32)]
 
 
+class _CacheArray(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
+
+
+class _Evict(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64), ("new_weight", ctypes.c_void_p),
+                ("new_weight_stride", ctypes.c_int64), ("keep", ctypes.c_int32), ("sink", ctypes.c_int32),
+                ("recent", ctypes.c_int32), ("new_table", ctypes.c_void_p), ("new_max_blocks", ctypes.c_int32),
+                ("new_num_blocks", ctypes.c_int32), ("arrays", ctypes.POINTER(_CacheArray)),
+                ("n_arrays", ctypes.c_int32)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -158,6 +172,8 @@ def load_library():
     lib.dsa_attn_weight.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_attn_weight.restype = ctypes.c_int
+    lib.dsa_cache_evict.argtypes = [P(_Batch), P(_Evict), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    lib.dsa_cache_evict.restype = ctypes.c_int
     lib.dsa_status_str.argtypes = [ctypes.c_int32]
     lib.dsa_status_str.restype = ctypes.c_char_p
     lib.dsa_version.restype = ctypes.c_char_p
@@ -711,6 +727,49 @@ def dsa_attn_weight(batch: Batch, q, kv_cache, sm_scale: float, lse, weight, *, 
     if rc != 0:
         raise DsaError(rc, "dsa_attn_weight")
     return weight
+
+
+def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arrays, *, sink: int = 0, recent: int = 0,
+                    new_weight=None, out_idx=None, out_len=None, workspace: Optional[Workspace] = None, stream=None):
+    """Keeps `keep` positions of each sequence: the first `sink`, the last `recent`, then those
+    with the largest weight [B, >= max_seq_len] fp32.  Copies their rows, in ascending order, from
+    each of `arrays` ([num_blocks, 64, ...], any type: latent rows, index keys, their scales) to
+    the pages new_table [B, n] int32 of the tensor at the same place in `new_arrays`
+    ([new blocks, 64, ...], as many for each), and their weights to new_weight.  Returns (idx
+    [B, keep] int32, -1 padded; len [B] int32)."""
+    lib = load_library()
+    dev = weight.get_device() if isinstance(weight, torch.Tensor) else -1
+    n = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 2 else None
+    cb = _batch_struct(batch, max(1, batch.max_q_per_seq), dev)
+    B = cb.batch
+    wp = _dense(weight, "weight", torch.float32, (B, n), dev)
+    W = new_table.shape[1] if isinstance(new_table, torch.Tensor) and new_table.dim() == 2 else None
+    tp = _dense(new_table, "new_table", torch.int32, (B, W), dev)
+    if len(arrays) != len(new_arrays):
+        raise ValueError(f"{len(arrays)} arrays, {len(new_arrays)} new ones")
+    new_blocks = int(new_arrays[0].shape[0]) if len(new_arrays) else max(1, B * W)
+    copies = (_CacheArray * max(1, len(arrays)))()
+    for i, (a, c) in enumerate(zip(arrays, new_arrays)):
+        ap = _dense(a, f"arrays[{i}]", a.dtype, (batch.num_blocks, 64) + tuple(a.shape[2:]), dev)
+        cp = _dense(c, f"new_arrays[{i}]", a.dtype, (new_blocks, 64) + tuple(a.shape[2:]), dev)
+        copies[i] = _CacheArray(ap, cp, a[0, 0].numel() * a.element_size())
+    np_, nn = None, 0
+    if new_weight is not None:
+        nn = new_weight.shape[1] if isinstance(new_weight, torch.Tensor) and new_weight.dim() == 2 else None
+        np_ = _dense(new_weight, "new_weight", torch.float32, (B, nn), dev)
+    s = _Evict(wp, n, np_, nn, keep, sink, recent, tp, W, new_blocks, copies, len(arrays))
+    status = _ptr((workspace if workspace is not None else status_workspace(weight.device)).get(256))
+    with _On(dev, stream) as on:
+        if out_idx is None:
+            out_idx = torch.empty((B, max(keep, 0)), dtype=torch.int32, device=weight.device)
+        if out_len is None:
+            out_len = torch.empty(B, dtype=torch.int32, device=weight.device)
+        ip = _dense(out_idx, "out_idx", torch.int32, (B, max(keep, 0)), dev)
+        lp = _dense(out_len, "out_len", torch.int32, (B,), dev)
+        rc = lib.dsa_cache_evict(ctypes.byref(cb), ctypes.byref(s), ip, lp, status, on)
+    if rc != 0:
+        raise DsaError(rc, "dsa_cache_evict")
+    return out_idx, out_len
 
 
 def decode_launch_count(batch: Batch, q_idx, w, k_cache, q, kv_cache, K: int, sm_scale: float,
