@@ -504,9 +504,10 @@ typedef struct {
     int32_t n_arrays;           /* 0..8                                                                */
 } dsa_evict_inputs;
 
-/* Two launches (one when there is nothing to copy); status as for dsa_chunk_attn, errors too. */
+/* status, scratch (dsa_evict_scratch_size bytes) and errors as for dsa_chunk_attn. */
+DSA_API size_t dsa_evict_scratch_size(const dsa_batch* batch);
 DSA_API dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, int32_t* out_idx, int32_t* out_len,
-                                   void* status, void* stream);
+                                   void* status, void* scratch, size_t scratch_bytes, void* stream);
 
 /* Static description of a status code. */
 DSA_API const char* dsa_status_str(int32_t status);

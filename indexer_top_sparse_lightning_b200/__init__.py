@@ -172,7 +172,10 @@ def load_library():
     lib.dsa_attn_weight.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_attn_weight.restype = ctypes.c_int
-    lib.dsa_cache_evict.argtypes = [P(_Batch), P(_Evict), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    lib.dsa_evict_scratch_size.argtypes = [P(_Batch)]
+    lib.dsa_evict_scratch_size.restype = ctypes.c_size_t
+    lib.dsa_cache_evict.argtypes = [P(_Batch), P(_Evict), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_cache_evict.restype = ctypes.c_int
     lib.dsa_status_str.argtypes = [ctypes.c_int32]
     lib.dsa_status_str.restype = ctypes.c_char_p
@@ -766,7 +769,9 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
             out_len = torch.empty(B, dtype=torch.int32, device=weight.device)
         ip = _dense(out_idx, "out_idx", torch.int32, (B, max(keep, 0)), dev)
         lp = _dense(out_len, "out_len", torch.int32, (B,), dev)
-        rc = lib.dsa_cache_evict(ctypes.byref(cb), ctypes.byref(s), ip, lp, status, on)
+        need = lib.dsa_evict_scratch_size(ctypes.byref(cb))
+        scratch = torch.empty(max(need, 256), dtype=torch.uint8, device=weight.device)
+        rc = lib.dsa_cache_evict(ctypes.byref(cb), ctypes.byref(s), ip, lp, status, scratch.data_ptr(), need, on)
     if rc != 0:
         raise DsaError(rc, "dsa_cache_evict")
     return out_idx, out_len

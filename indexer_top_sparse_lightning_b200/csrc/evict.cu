@@ -1,5 +1,5 @@
-// evict.cu -- host side of dsa_cache_evict (include/dsa.h): argument checks and the
-// two launches.
+// evict.cu -- host side of dsa_cache_evict (include/dsa.h): argument checks, scratch
+// and launches.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -46,9 +46,32 @@ dsa_status check_evict(const dsa_batch* bt, const dsa_evict_inputs* in, const in
 
 }  // namespace
 
-extern "C" dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, int32_t* out_idx, int32_t* out_len,
-                                      void* status, void* stream) {
+namespace {
+
+// CTAs per sequence of the wide kernels (0: the cluster kernel serves), and their scratch.
+int wide_ctas(const dsa_batch* bt, const DevInfo& di) {
+    if (bt->max_seq_len < kEvictWide) return 0;
+    const int by_len = (bt->max_seq_len + kEvictWideRange - 1) / kEvictWideRange;
+    const int by_sms = di.sms / bt->batch > 8 ? di.sms / bt->batch : 8;
+    return by_len < by_sms ? by_len : by_sms;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_evict_scratch_size(const dsa_batch* batch) {
+    if (check_batch(batch) != DSA_OK) return 0;
+    const DevInfo di = dev_info();
+    if (di.sms <= 0) return 0;
+    return 256 + align256((size_t)batch->batch * (3 * kEvictBins + 2 * (size_t)wide_ctas(batch, di)) * 4);
+}
+
+dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, int32_t* out_idx, int32_t* out_len, void* status,
+                           void* scratch, size_t scratch_bytes, void* stream) {
     if (dsa_status st = check_evict(batch, in, out_idx, out_len, status)) return st;
+    if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < dsa_evict_scratch_size(batch))
+        return DSA_ERR_WORKSPACE;
     const DevInfo di = dev_info();
     if (di.sms <= 0) return fail(DSA_ERR_CUDA, "device query failed");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -84,30 +107,44 @@ extern "C" dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_in
         e.pieces = (int32_t)(a.row_bytes / e.width);
         e.magic = (uint32_t)(((uint64_t(1) << 32) + e.pieces - 1) / e.pieces);
     }
-    p.cluster = 1;
-    while (p.cluster < 8 && (int64_t)p.cluster * 8192 < batch->max_seq_len) p.cluster *= 2;
-    const int per = (batch->max_seq_len + p.cluster - 1) / p.cluster;
-    p.cache = per <= kEvictCache ? per : 0;
-    const int smem = (int)sizeof(EvictShared) + p.cache * 4;
-    if (di.max_smem < smem) return fail(DSA_ERR_UNSUPPORTED, "device shared memory per block too small");
-    if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(&evict_select_kernel), (int)sizeof(EvictShared) + kEvictCache * 4))
-        return fail(DSA_ERR_CUDA, "shared memory attribute", e);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)(p.B * p.cluster), 1, 1);
     cfg.blockDim = dim3(kEvictThreads, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaError_t e = cudaLaunchKernelEx(&cfg, &evict_select_kernel, p)) return fail(DSA_ERR_CUDA, "eviction choice launch", e);
+    p.ctas = wide_ctas(batch, di);
+    if (p.ctas) {
+        p.hist = static_cast<uint32_t*>(scratch);
+        p.counts = p.hist + (size_t)p.B * 3 * kEvictBins;
+        if (cudaError_t e = cudaMemsetAsync(p.hist, 0, (size_t)p.B * 3 * kEvictBins * 4, s))
+            return fail(DSA_ERR_CUDA, "eviction histogram clear", e);
+        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)p.B, 1);
+        void (*const steps[5])(EvictParams) = {&evict_wide_kernel<0>, &evict_wide_kernel<1>, &evict_wide_kernel<2>,
+                                               &evict_wide_kernel<3>, &evict_wide_kernel<4>};
+        for (int i = 0; i < 5; ++i) {
+            cfg.numAttrs = i == 0 ? 0 : 1;      // (the first follows the clear in stream order)
+            if (cudaError_t e = cudaLaunchKernelEx(&cfg, steps[i], p)) return fail(DSA_ERR_CUDA, "eviction choice launch", e);
+        }
+    } else {
+        p.cluster = 1;
+        while (p.cluster < 8 && (int64_t)p.cluster * 8192 < batch->max_seq_len) p.cluster *= 2;
+        p.cache = (batch->max_seq_len + p.cluster - 1) / p.cluster;
+        const int smem = (int)sizeof(EvictShared) + p.cache * 4;
+        if (di.max_smem < smem) return fail(DSA_ERR_UNSUPPORTED, "device shared memory per block too small");
+        if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(&evict_select_kernel), (int)sizeof(EvictShared) + 8192 * 4))
+            return fail(DSA_ERR_CUDA, "shared memory attribute", e);
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)p.cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(p.B * p.cluster), 1, 1);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.numAttrs = 2;
+        if (cudaError_t e = cudaLaunchKernelEx(&cfg, &evict_select_kernel, p)) return fail(DSA_ERR_CUDA, "eviction choice launch", e);
+    }
     if (p.n_arrays == 0 && !p.new_weight) return DSA_OK;
     const int most = batch->max_seq_len < in->keep ? batch->max_seq_len : in->keep;
     cfg.gridDim = dim3((unsigned)((most + kEvictCopyRows - 1) / kEvictCopyRows), (unsigned)p.B, 1);
@@ -117,3 +154,5 @@ extern "C" dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_in
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, &evict_copy_kernel, p)) return fail(DSA_ERR_CUDA, "eviction copy launch", e);
     return DSA_OK;
 }
+
+}  // extern "C"

@@ -10,11 +10,15 @@
 // three digit histograms (11, 11 and 10 bits of the order-preserving key), each
 // joined over the cluster through distributed shared memory; then the keys above
 // it, and as many equal to it as are wanted, lowest positions first, are written
-// with counts and ballots in position order.  Ranges of up to kEvictCache
-// positions stay in shared memory as keys; longer ones are read again (from L2)
-// by each of the five passes.  Weights of zero (positions nobody attends to) are
+// with counts and ballots in position order.  A range's keys stay in shared
+// memory.  Weights of zero (positions nobody attends to) are
 // common: they are counted with ballots, since a histogram bin that a whole warp
 // adds to takes its lanes one by one.
+//
+// Longer sequences (kEvictWide positions and more) take the same steps as launches of
+// their own over many CTAs (evict_wide_kernel: three digits, counts, lists), joined
+// through histograms in scratch: eight CTAs would need 270 us for a million
+// positions, most of it histogram adds, which a CTA takes one by one.
 //
 // evict_copy_kernel: memory-bound, every kept row read and written once.  A block
 // takes 32 rows: their places are resolved once, then each array's rows are copied
@@ -27,9 +31,11 @@
 namespace dsa {
 
 constexpr int kEvictThreads = 1024;
-constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictCache = 45056;          // keys that a CTA keeps in shared memory (176 KB)
+constexpr int kEvictWarps = kEvictThreads / 32;   // a warp's lanes
+static_assert(kEvictWarps == 32, "one lane per warp in the sums over warps");
 constexpr int kEvictBins = 2048;
+constexpr int kEvictWide = 65537;           // longest sequence from which the wide kernels are used
+constexpr int kEvictWideRange = 4096;       // positions per CTA there, at least
 constexpr int kEvictMaxArrays = 8;
 constexpr int kEvictCopyThreads = 256;
 constexpr int kEvictCopyRows = 32;
@@ -57,8 +63,13 @@ struct EvictParams {
     int32_t new_max_blocks, new_num_blocks;
     int32_t keep, sink, recent;
     int32_t cluster;          // CTAs per sequence
-    int32_t cache;            // keys of a CTA's range that fit its shared memory (0: none are kept)
+    int32_t cache;            // keys of a CTA's range at most (in shared memory)
     int32_t n_arrays;
+    // the wide kernels: CTAs per sequence, and [B][3][2048] digit counts (zero at first), then
+    // [B][ctas][2] counts of keys above and equal
+    int32_t ctas;
+    uint32_t* hist;
+    uint32_t* counts;
     EvictArray arrays[kEvictMaxArrays];
 };
 
@@ -77,6 +88,16 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32
     return v;
 }
 
+// Sum of the entries of the warps before this one.
+__device__ __forceinline__ uint32_t sum_before(const uint32_t* per_warp) {
+    const uint32_t lane = threadIdx.x & 31;
+    return __reduce_add_sync(0xffffffffu, lane < threadIdx.x >> 5 ? per_warp[lane] : 0u);
+}
+// ... of all warps.
+__device__ __forceinline__ uint32_t sum_all(const uint32_t* per_warp) {
+    return __reduce_add_sync(0xffffffffu, per_warp[threadIdx.x & 31]);
+}
+
 // Length of sequence b as the kernels use it; out-of-range lengths are cut (and reported).
 __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
     const int L = __ldg(p.seq_lens + b);
@@ -85,6 +106,38 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
         return L < 0 ? 0 : p.max_len;
     }
     return L;
+}
+
+// Writes the positions that stay of this warp's range [w0, w1), in order, behind those of
+// the warps and CTAs before.
+template <typename Key>
+__device__ __forceinline__ void evict_emit(const EvictShared* s, int32_t* out, int lo, int w0, int w1, uint32_t prefix,
+                                           uint32_t need, Key key_at) {
+    constexpr int BATCH = 8;
+    const int lane = threadIdx.x & 31;
+    const uint32_t g = s->gt_before + sum_before(s->warp_gt);
+    uint32_t e = s->eq_before + sum_before(s->warp_eq);
+    uint32_t at = g + (e < need ? e : need);
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i0 = w0; i0 < w1; i0 += 32 * BATCH) {
+        uint32_t k[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int i = i0 + 32 * u + lane;
+            k[u] = i < w1 ? key_at(i) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int i = i0 + 32 * u + lane;
+            const bool in = i < w1;
+            const uint32_t me = __ballot_sync(0xffffffffu, in && k[u] == prefix);
+            const bool sel = in && (k[u] > prefix || (k[u] == prefix && e + __popc(me & below) < need));
+            const uint32_t ms = __ballot_sync(0xffffffffu, sel);
+            if (sel) out[at + __popc(ms & below)] = lo + i;
+            at += __popc(ms);
+            e += __popc(me);
+        }
+    }
 }
 
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
@@ -110,7 +163,6 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
     const int lo = lo64 < L ? (int)lo64 : L;
     const int n = L - lo < per ? L - lo : per;           // this CTA's positions lo .. lo + n - 1
     const float* w = p.weight + (int64_t)b * p.stride + lo;
-    const bool cached = n <= p.cache;
     // Keys compare like weights; NaN lies below everything, positions that stay in any case above.
     auto make_key = [&](int i) -> uint32_t {
         const float x = __ldg(w + i);
@@ -118,7 +170,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
         if (pos < p.sink || pos >= L - p.recent) return 0xFFFFFFFFu;
         return x != x ? 0u : order_key(x);
     };
-    auto key_at = [&](int i) -> uint32_t { return cached ? s_key[i] : make_key(i); };
+    auto key_at = [&](int i) -> uint32_t { return s_key[i]; };
     constexpr uint32_t ZERO = 0x80000000u;               // order_key(0)
     constexpr int BATCH = 8;
 
@@ -142,7 +194,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
 #pragma unroll
             for (int u = 0; u < BATCH; ++u) {
                 const int i = i0 + u * kEvictThreads + (int)threadIdx.x;
-                if (in[u] && pass == 0 && cached) s_key[i] = k[u];
+                if (in[u] && pass == 0) s_key[i] = k[u];
                 const bool here = in[u] && (k[u] & above_mask) == prefix;
                 const uint32_t z = __ballot_sync(0xffffffffu, here && k[u] == ZERO);
                 zeros += __popc(z);
@@ -167,7 +219,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
         if (lane == 31) s->warp_sum[warp] = x;
         __syncthreads();
         uint32_t before = x - (c1 + c0);
-        for (int q = 0; q < warp; ++q) before += s->warp_sum[q];
+        before += sum_before(s->warp_sum);
         // keys in bins above bin1: `before`; the wanted key's bin holds the need-th
         if (before < need && need <= before + c1) {
             s->digit = (uint32_t)bin1;
@@ -204,14 +256,12 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
         s->warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        uint32_t g = 0, e = 0;
-        for (int q = 0; q < kEvictWarps; ++q) {
-            g += s->warp_gt[q];
-            e += s->warp_eq[q];
+    if (warp == 0) {
+        const uint32_t g = sum_all(s->warp_gt), e = sum_all(s->warp_eq);
+        if (lane == 0) {
+            s->cta_gt = g;
+            s->cta_eq = e;
         }
-        s->cta_gt = g;
-        s->cta_eq = e;
     }
     cluster_sync();
     if (threadIdx.x == 0) {
@@ -224,30 +274,145 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
         s->eq_before = e;
     }
     cluster_sync();          // (no CTA leaves while another reads its counts)
-    uint32_t g = s->gt_before, e = s->eq_before;
-    for (int q = 0; q < warp; ++q) {
-        g += s->warp_gt[q];
-        e += s->warp_eq[q];
+    evict_emit(s, out, lo, w0, w1, prefix, need, key_at);
+}
+
+// The wide kernels.  STEP 0..2: the histogram of a digit among the keys that share
+// the digits before; 3: the keys above and equal to the threshold in this CTA's
+// range; 4: the list.  Every step finds the digits again from the histograms.
+template <int STEP>
+__global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __grid_constant__ EvictParams p) {
+    __shared__ EvictShared s_all;
+    EvictShared* s = &s_all;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = (int)blockIdx.y, cta = (int)blockIdx.x;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int L = evict_len(p, b), keep = p.keep;
+    int32_t* out = p.idx + (int64_t)b * keep;
+    if (STEP == 4 && cta == 0 && threadIdx.x == 0) p.len[b] = L < keep ? L : keep;
+    if (L <= keep) {
+        if (STEP == 4)
+            for (int64_t i = (int64_t)cta * kEvictThreads + threadIdx.x; i < keep; i += (int64_t)p.ctas * kEvictThreads)
+                out[i] = i < L ? (int32_t)i : -1;
+        return;
     }
-    uint32_t at = g + (e < need ? e : need);
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32 * BATCH) {
-        uint32_t k[BATCH];
+    const int per = (L + p.ctas - 1) / p.ctas;
+    const int64_t lo64 = (int64_t)per * cta;
+    const int lo = lo64 < L ? (int)lo64 : L;
+    const int n = L - lo < per ? L - lo : per;
+    const float* w = p.weight + (int64_t)b * p.stride + lo;
+    auto key_at = [&](int i) -> uint32_t {
+        const float x = __ldg(w + i);
+        const int pos = lo + i;
+        if (pos < p.sink || pos >= L - p.recent) return 0xFFFFFFFFu;
+        return x != x ? 0u : order_key(x);
+    };
+    constexpr uint32_t ZERO = 0x80000000u;               // order_key(0)
+    constexpr int BATCH = 4;
+    constexpr int SHIFT[3] = {21, 10, 0};
+    uint32_t* hist = p.hist + (int64_t)b * 3 * kEvictBins;
+
+    uint32_t prefix = 0, need = (uint32_t)keep;
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int i = i0 + 32 * u + lane;
-            k[u] = i < w1 ? key_at(i) : 0u;
+    for (int d = 0; d < (STEP < 3 ? STEP : 3); ++d) {
+        const int bin1 = kEvictBins - 1 - 2 * (int)threadIdx.x, bin0 = bin1 - 1;
+        const uint32_t c1 = __ldcg(hist + d * kEvictBins + bin1), c0 = __ldcg(hist + d * kEvictBins + bin0);
+        uint32_t x = c1 + c0;
+#pragma unroll
+        for (int e = 1; e < 32; e <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, e);
+            if (lane >= e) x += y;
         }
+        if (lane == 31) s->warp_sum[warp] = x;
+        __syncthreads();
+        uint32_t before = x - (c1 + c0);
+        before += sum_before(s->warp_sum);
+        if (before < need && need <= before + c1) {
+            s->digit = (uint32_t)bin1;
+            s->above = before;
+        } else if (before + c1 < need && need <= before + c1 + c0) {
+            s->digit = (uint32_t)bin0;
+            s->above = before + c1;
+        }
+        __syncthreads();
+        prefix |= s->digit << SHIFT[d];
+        need -= s->above;
+        __syncthreads();
+    }
+    if constexpr (STEP < 3) {
+        constexpr uint32_t above_mask = STEP == 0 ? 0u : STEP == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+        constexpr uint32_t mask = STEP == 2 ? 1023u : 2047u;
+        for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads) s->hist[i] = 0;
+        __syncthreads();
+        uint32_t zeros = 0;
+        for (int i0 = 0; i0 < n; i0 += kEvictThreads * BATCH) {
+            uint32_t k[BATCH];
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int i = i0 + 32 * u + lane;
-            const bool in = i < w1;
-            const uint32_t me = __ballot_sync(0xffffffffu, in && k[u] == prefix);
-            const bool sel = in && (k[u] > prefix || (k[u] == prefix && e + __popc(me & below) < need));
-            const uint32_t ms = __ballot_sync(0xffffffffu, sel);
-            if (sel) out[at + __popc(ms & below)] = lo + i;
-            at += __popc(ms);
-            e += __popc(me);
+            for (int u = 0; u < BATCH; ++u) {
+                const int i = i0 + u * kEvictThreads + (int)threadIdx.x;
+                k[u] = i < n ? key_at(i) : 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const bool here = i0 + u * kEvictThreads + (int)threadIdx.x < n && (k[u] & above_mask) == prefix;
+                zeros += __popc(__ballot_sync(0xffffffffu, here && k[u] == ZERO));
+                if (here && k[u] != ZERO) atomicAdd(&s->hist[(k[u] >> SHIFT[STEP]) & mask], 1u);
+            }
+        }
+        if (lane == 0 && zeros) atomicAdd(&s->hist[(ZERO >> SHIFT[STEP]) & mask], zeros);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads)
+            if (s->hist[i]) atomicAdd(hist + STEP * kEvictBins + i, s->hist[i]);
+    } else {
+        const int span = (n + kEvictWarps - 1) / kEvictWarps;
+        const int w0 = warp * span < n ? warp * span : n, w1 = w0 + span < n ? w0 + span : n;
+        uint32_t gt = 0, eq = 0;
+        for (int i0 = w0; i0 < w1; i0 += 32 * BATCH) {
+            uint32_t k[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int i = i0 + 32 * u + lane;
+                k[u] = i < w1 ? key_at(i) : 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const bool in = i0 + 32 * u + lane < w1;
+                gt += __popc(__ballot_sync(0xffffffffu, in && k[u] > prefix));
+                eq += __popc(__ballot_sync(0xffffffffu, in && k[u] == prefix));
+            }
+        }
+        if (lane == 0) {
+            s->warp_gt[warp] = gt;
+            s->warp_eq[warp] = eq;
+        }
+        __syncthreads();
+        if constexpr (STEP == 3) {
+            const uint32_t g = sum_all(s->warp_gt), e = sum_all(s->warp_eq);
+            if (threadIdx.x == 0) {
+                p.counts[2 * ((int64_t)b * p.ctas + cta)] = g;
+                p.counts[2 * ((int64_t)b * p.ctas + cta) + 1] = e;
+            }
+        } else {
+            // counts of the CTAs before, then of the warps before
+            if (warp == 0) {
+                uint32_t g = 0, e = 0;
+                for (int q = lane; q < cta; q += 32) {
+                    g += __ldcg(p.counts + 2 * ((int64_t)b * p.ctas + q));
+                    e += __ldcg(p.counts + 2 * ((int64_t)b * p.ctas + q) + 1);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) {
+                    g += __shfl_xor_sync(0xffffffffu, g, d);
+                    e += __shfl_xor_sync(0xffffffffu, e, d);
+                }
+                if (lane == 0) {
+                    s->gt_before = g;
+                    s->eq_before = e;
+                }
+            }
+            __syncthreads();
+            evict_emit(s, out, lo, w0, w1, prefix, need, key_at);
         }
     }
 }
@@ -277,7 +442,7 @@ __device__ __forceinline__ void evict_copy_rows(const EvictArray& a, const int64
     }
 }
 
-__global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kEvictCopyThreads, 6) evict_copy_kernel(const __grid_constant__ EvictParams p) {
     __shared__ int64_t s_src[kEvictCopyRows], s_dst[kEvictCopyRows];
     griddep_wait();
     const int b = (int)blockIdx.y;

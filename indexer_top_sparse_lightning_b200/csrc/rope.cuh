@@ -154,7 +154,7 @@ __device__ __forceinline__ void turned8(const uint16_t* x, uint4 v, int e, const
 // row, kRopeGroups rows at a time); the blocks behind them: the key rows of
 // ktpc tokens each.  Query blocks of one token's heads share its angle table.
 template <int NV>
-__global__ void __launch_bounds__(kRopeThreads, NV <= 9 ? 3 : 2) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, NV <= 2 ? 6 : NV <= 4 ? 4 : NV <= 9 ? 3 : 2) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 s_cs[kRopeTable];
     __shared__ int s_seq[kRopeGroups];
     __shared__ int64_t s_pos[kRopeGroups];   // the token's place in its sequence
