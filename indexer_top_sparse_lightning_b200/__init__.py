@@ -560,7 +560,7 @@ class _On:
 
 def _dense(t, name, dtype, shape, dev: int) -> int:
     """Pointer of a dense tensor of this type, shape and device index; raises what is wrong with another."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 \
             and t.is_contiguous():
         return t.data_ptr()
     _check(t, name, dtype, len(shape), shape)

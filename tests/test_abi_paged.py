@@ -69,3 +69,89 @@ def test_rope_rejects_in_place_on_strided_queries(lib):
                                  dict(block_table=None), dict(num_blocks=0), dict(max_blocks_per_seq=0)])
 def test_rope_rejects_bad_batch(lib, bad):
     assert _call_rope(lib, batch=_batch(**bad)) == INVALID
+
+
+def _attn(**kw):
+    d = dict(q=16, kv_cache=16, H=128, sm_scale=0.04, kv_dtype=0, kv_scale=None)
+    d.update(kw)
+    return dsa._Attn(**d)
+
+
+def _call_chunk(lib, batch=None, out=16, lse=None, status=256, scratch=256, nbytes=1 << 40, **kw):
+    return lib.dsa_chunk_attn(ctypes.byref(batch if batch is not None else _batch()), ctypes.byref(_attn(**kw)), out, lse,
+                              status, scratch, nbytes, None)
+
+
+def _call_weight(lib, batch=None, lse=16, weight=16, stride=64, decay=1.0, status=256, scratch=256, nbytes=1 << 40, **kw):
+    return lib.dsa_attn_weight(ctypes.byref(batch if batch is not None else _batch()), ctypes.byref(_attn(**kw)), lse, weight,
+                               stride, decay, status, scratch, nbytes, None)
+
+
+BAD_ATTN = [(dict(H=0), UNSUPPORTED), (dict(H=129), UNSUPPORTED), (dict(q=None), INVALID), (dict(q=8), INVALID),
+            (dict(kv_cache=None), INVALID), (dict(sm_scale=0.0), INVALID), (dict(sm_scale=float("nan")), INVALID),
+            (dict(kv_dtype=2), INVALID), (dict(kv_dtype=1), INVALID), (dict(kv_dtype=1, kv_scale=18), INVALID)]
+BAD_BATCH = [dict(batch=0), dict(num_tokens=0), dict(seq_lens=None), dict(cu_q=None), dict(block_table=None),
+             dict(num_blocks=0), dict(max_seq_len=65), dict(max_seq_len=0), dict(max_q_per_seq=0)]
+
+
+@pytest.mark.parametrize("bad,code", BAD_ATTN)
+def test_dense_operators_reject_bad_inputs(lib, bad, code):
+    assert _call_chunk(lib, **bad) == code
+    assert _call_weight(lib, **bad) == code
+    assert lib.dsa_chunk_scratch_size(ctypes.byref(_batch()), ctypes.byref(_attn(**bad))) == 0
+    assert lib.dsa_weight_scratch_size(ctypes.byref(_batch()), ctypes.byref(_attn(**bad))) == 0
+
+
+@pytest.mark.parametrize("bad", BAD_BATCH)
+def test_dense_operators_reject_bad_batches(lib, bad):
+    assert _call_chunk(lib, batch=_batch(**bad)) == INVALID
+    assert _call_weight(lib, batch=_batch(**bad)) == INVALID
+    assert _call_evict(lib, batch=_batch(**bad)) == INVALID
+    assert lib.dsa_evict_scratch_size(ctypes.byref(_batch(**bad))) == 0
+
+
+def test_dense_operators_reject_more_rows_than_32_bits_count(lib):
+    many = _batch(num_tokens=2 ** 24)
+    assert _call_chunk(lib, batch=many) == UNSUPPORTED
+    assert _call_weight(lib, batch=many) == UNSUPPORTED
+
+
+def _call_evict(lib, batch=None, idx=16, length=16, status=256, scratch=256, nbytes=1 << 40, arrays=None, **kw):
+    rows = (dsa._CacheArray * 16)(*(arrays or [(16, 16, 1152)]))
+    d = dict(weight=16, weight_stride=64, new_weight=None, new_weight_stride=0, keep=32, sink=0, recent=0, new_table=16,
+             new_max_blocks=1, new_num_blocks=1, arrays=rows, n_arrays=len(arrays or [1]))
+    d.update(kw)
+    return lib.dsa_cache_evict(ctypes.byref(batch if batch is not None else _batch()), ctypes.byref(dsa._Evict(**d)), idx, length,
+                               status, scratch, nbytes, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(weight=None), INVALID), (dict(weight_stride=63), INVALID), (dict(keep=0), INVALID), (dict(sink=-1), INVALID),
+    (dict(recent=-1), INVALID), (dict(sink=16, recent=17), INVALID), (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), INVALID),
+    (dict(new_table=None), INVALID), (dict(new_max_blocks=0), INVALID), (dict(new_num_blocks=0), INVALID),
+    (dict(new_weight=32, new_weight_stride=31), INVALID), (dict(new_weight=16, new_weight_stride=64), INVALID),
+    (dict(n_arrays=-1), INVALID), (dict(n_arrays=9), UNSUPPORTED), (dict(idx=None), INVALID), (dict(length=None), INVALID),
+    (dict(status=None), INVALID), (dict(arrays=[(None, 16, 1152)]), INVALID), (dict(arrays=[(16, None, 1152)]), INVALID),
+    (dict(arrays=[(16, 16, 0)]), INVALID), (dict(arrays=[(16, 16, 2049)]), UNSUPPORTED),
+])
+def test_evict_rejects_bad_inputs(lib, bad, code):
+    assert _call_evict(lib, **bad) == code
+
+
+def test_python_entry_points_want_cuda_tensors():
+    import torch
+    t = torch.zeros(1, dtype=torch.int32)
+    b = dsa.Batch(t, torch.zeros(2, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32), 1, 1, 1)
+    q, kv = torch.zeros(1, 2, 576, dtype=torch.bfloat16), torch.zeros(1, 64, 576, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dsa.dsa_qk_norm_rope(b, None, q)
+    with pytest.raises(ValueError):
+        dsa.dsa_qk_norm_rope(b, None)
+    with pytest.raises(ValueError):
+        dsa.dsa_chunk_attn(b, q, kv, 0.04)
+    with pytest.raises(ValueError):
+        dsa.dsa_attn_weight(b, q, kv, 0.04, torch.zeros(1, 2), torch.zeros(1, 1))
+    with pytest.raises(ValueError):
+        dsa.dsa_cache_evict(b, torch.zeros(1, 1), 1, t.view(1, 1), [], [])
+    with pytest.raises(TypeError):
+        dsa.dsa_chunk_attn(b, None, kv, 0.04)
