@@ -331,7 +331,9 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 const int kr = g % Cfg::KRING;
                 if (!elected_wait(el, &m->k_empty[kr], ph, abort, wlim)) return false;
                 if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[kr], bytes);
-                if (mine) tma_load_3d_pair(s_k + kr * Cfg::KGROUP, &tm_k, k_lead + 8 * kr, 0, y, 3 * g);
+                // (fp16: the small rests first, so that adding them up costs no bits of the sum)
+                const int chunk = F16 && g < Cfg::KRING ? 3 * g + 9 : F16 ? 3 * g - 9 : 3 * g;
+                if (mine) tma_load_3d_pair(s_k + kr * Cfg::KGROUP, &tm_k, k_lead + 8 * kr, 0, y, chunk);
                 if (kr == Cfg::KRING - 1) ph ^= 1;
             }
             return true;

@@ -234,11 +234,13 @@ __global__ void __launch_bounds__(WeightCfg<NR>::THREADS, 1)
                     // a page that nobody sees is not loaded: its positions' sums are not used
                     if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[r], pages * Cfg::GROUP * (Cfg::CHUNK / 2));
                     uint8_t* dst = s_k + r * (Cfg::GROUP * Cfg::CHUNK);
+                    // (fp16: the small rests first, so that adding them up costs no bits of the sum)
+                    const int z = F16 ? (c < 9 ? c + 9 : c - 9) : c;
 #pragma unroll
                     for (int j = 0; j < Cfg::GROUP; ++j) {
-                        if (el && i0 >= 0) tma_load_3d_pair(dst + j * Cfg::CHUNK, &tm_k, lead + 8 * r, 0, i0 * kPage, c + j);
+                        if (el && i0 >= 0) tma_load_3d_pair(dst + j * Cfg::CHUNK, &tm_k, lead + 8 * r, 0, i0 * kPage, z + j);
                         if (el && i1 >= 0)
-                            tma_load_3d_pair(dst + j * Cfg::CHUNK + Cfg::CHUNK / 2, &tm_k, lead + 8 * r, 0, i1 * kPage, c + j);
+                            tma_load_3d_pair(dst + j * Cfg::CHUNK + Cfg::CHUNK / 2, &tm_k, lead + 8 * r, 0, i1 * kPage, z + j);
                     }
                     if (++r == Cfg::RING) {
                         r = 0;
