@@ -492,7 +492,7 @@ typedef struct {
 typedef struct {
     const float* weight;        /* device [B, weight_stride], weight_stride >= max_seq_len             */
     int64_t weight_stride;
-    float* new_weight;          /* device [B, new_weight_stride] or NULL; not weight itself            */
+    float* new_weight;          /* device [B, new_weight_stride] or NULL; apart from weight             */
     int64_t new_weight_stride;  /* >= min(keep, max_seq_len)                                           */
     int32_t keep;               /* positions that stay, >= 1                                           */
     int32_t sink;               /* first positions that stay in any case, >= 0                         */

@@ -521,16 +521,28 @@ def status_workspace(device=None) -> Workspace:
     """The default status area of the dsa_ operators over the paged cache on a
     device: read it with get_status(status_workspace(device)).  It keeps its address for
     the life of the process, so captured graphs may hold it."""
-    key = None if device is None else torch.device(device).index
+    key = device if isinstance(device, int) else None if device is None else torch.device(device).index
     if key is None:
         key = torch.cuda.current_device()
     if key not in _status_ws:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the default status area is not there yet: call status_workspace() before the capture")
         ws = Workspace(torch.device("cuda", key))
         ws.get(256)
         # zeroed before any stream can use it
         torch.cuda.synchronize(ws.device)
         _status_ws[key] = ws
     return _status_ws[key]
+
+
+def _status(ws: Optional[Workspace], dev: int) -> int:
+    """Pointer of a call's status area, on the device that is current."""
+    if ws is None:
+        return status_workspace(dev).get(256).data_ptr()
+    t = ws.get(256)
+    if t.get_device() != dev:
+        raise ValueError(f"the workspace is on {t.device}, the tensors on cuda:{dev}")
+    return t.data_ptr()
 
 
 class _On:
@@ -651,8 +663,8 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
     cb = _batch_struct(batch, T, dev)
     s = _Rope(qp, qs[0], qs[1], kp, ks[0], H, D, qg, kg, qn, kn, eps, fp, R,
               D - R if rope_off is None else rope_off, bool(interleaved), pp, kt)
-    status = _ptr((workspace if workspace is not None else status_workspace(main.device)).get(256))
     with _On(dev, stream) as on:
+        status = _status(workspace, dev)
         op = 0
         if q is not None:
             if q_out is None:
@@ -691,8 +703,8 @@ def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None,
     lib = load_library()
     at, T, H, dev = _latent_attn(q, kv_cache, sm_scale, kv_scale, batch.num_blocks)
     cb = _batch_struct(batch, T, dev)
-    status = _ptr((workspace if workspace is not None else status_workspace(q.device)).get(256))
     with _On(dev, stream) as on:
+        status = _status(workspace, dev)
         need = lib.dsa_chunk_scratch_size(ctypes.byref(cb), ctypes.byref(at))
         if need == 0:
             raise DsaError(2, "dsa_chunk_scratch_size")
@@ -720,8 +732,8 @@ def dsa_attn_weight(batch: Batch, q, kv_cache, sm_scale: float, lse, weight, *, 
     lp = _dense(lse, "lse", torch.float32, (T, H), dev)
     n = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 2 else None
     wp = _dense(weight, "weight", torch.float32, (cb.batch, n), dev)
-    status = _ptr((workspace if workspace is not None else status_workspace(q.device)).get(256))
     with _On(dev, stream) as on:
+        status = _status(workspace, dev)
         need = lib.dsa_weight_scratch_size(ctypes.byref(cb), ctypes.byref(at))
         if need == 0:
             raise DsaError(2, "dsa_weight_scratch_size")
@@ -748,11 +760,15 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
     wp = _dense(weight, "weight", torch.float32, (B, n), dev)
     W = new_table.shape[1] if isinstance(new_table, torch.Tensor) and new_table.dim() == 2 else None
     tp = _dense(new_table, "new_table", torch.int32, (B, W), dev)
+    if keep < 0 or sink < 0 or recent < 0 or sink + recent > keep:
+        raise ValueError(f"keep {keep} has no room for sink {sink} and recent {recent}")
     if len(arrays) != len(new_arrays):
         raise ValueError(f"{len(arrays)} arrays, {len(new_arrays)} new ones")
     new_blocks = int(new_arrays[0].shape[0]) if len(new_arrays) else max(1, B * W)
     copies = (_CacheArray * max(1, len(arrays)))()
     for i, (a, c) in enumerate(zip(arrays, new_arrays)):
+        if not isinstance(a, torch.Tensor) or a.dim() < 2:
+            raise ValueError(f"arrays[{i}] must be a tensor [num_blocks, 64, ...]")
         ap = _dense(a, f"arrays[{i}]", a.dtype, (batch.num_blocks, 64) + tuple(a.shape[2:]), dev)
         cp = _dense(c, f"new_arrays[{i}]", a.dtype, (new_blocks, 64) + tuple(a.shape[2:]), dev)
         copies[i] = _CacheArray(ap, cp, a[0, 0].numel() * a.element_size())
@@ -761,13 +777,13 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
         nn = new_weight.shape[1] if isinstance(new_weight, torch.Tensor) and new_weight.dim() == 2 else None
         np_ = _dense(new_weight, "new_weight", torch.float32, (B, nn), dev)
     s = _Evict(wp, n, np_, nn, keep, sink, recent, tp, W, new_blocks, copies, len(arrays))
-    status = _ptr((workspace if workspace is not None else status_workspace(weight.device)).get(256))
     with _On(dev, stream) as on:
+        status = _status(workspace, dev)
         if out_idx is None:
-            out_idx = torch.empty((B, max(keep, 0)), dtype=torch.int32, device=weight.device)
+            out_idx = torch.empty((B, keep), dtype=torch.int32, device=weight.device)
         if out_len is None:
             out_len = torch.empty(B, dtype=torch.int32, device=weight.device)
-        ip = _dense(out_idx, "out_idx", torch.int32, (B, max(keep, 0)), dev)
+        ip = _dense(out_idx, "out_idx", torch.int32, (B, keep), dev)
         lp = _dense(out_len, "out_len", torch.int32, (B,), dev)
         need = lib.dsa_evict_scratch_size(ctypes.byref(cb))
         scratch = torch.empty(max(need, 256), dtype=torch.uint8, device=weight.device)

@@ -36,7 +36,7 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
     const int64_t rows = (int64_t)bt->num_tokens * at->H;
     const int64_t tiles = (rows + ChunkCfg::ROWS - 1) / ChunkCfg::ROWS +
                           (bt->batch < bt->num_tokens ? bt->batch : bt->num_tokens);
-    const int64_t blocks = tiles * ((bt->max_seq_len + ChunkCfg::BLOCK - 1) / ChunkCfg::BLOCK);
+    const int64_t blocks = tiles * (((int64_t)bt->max_seq_len + ChunkCfg::BLOCK - 1) / ChunkCfg::BLOCK);
     pl.pairs = (int)(blocks < pmax ? blocks : pmax);
     pl.copy_off = align256(ChunkCfg::HEAD_BYTES + (size_t)pmax * 4 * (size_t)ChunkCfg::PART_BYTES);
     pl.total = pl.copy_off;
@@ -82,7 +82,7 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     p.num_blocks = batch->num_blocks;
     p.staged = (int32_t)pl.pages;
     const int64_t room = (pl.pages ? pl.pages : (int64_t)batch->max_blocks_per_seq) * kPage;
-    p.max_len = (int32_t)(room < INT32_MAX ? room : INT32_MAX);
+    p.max_len = (int32_t)(room < kMaxLen ? room : kMaxLen);
     p.tokens = p.max_tokens = INT32_MAX;
     p.scale_log2 = at->sm_scale * 1.4426950408889634f;
     const void* rows = at->kv_cache;

@@ -7,6 +7,7 @@
 namespace dsa {
 
 constexpr int kPage = 64;             // tokens per cache page
+constexpr int kMaxLen = INT32_MAX - 4095;   // longest sequence: its blocks and ranges end below 2^31
 constexpr int kTileKeys = 128;        // keys per indexer MMA tile (two pages)
 constexpr int kMaxTopK = 2048;
 constexpr int kDqk = 576;             // latent 512 + RoPE 64

@@ -33,7 +33,12 @@ dsa_status check_evict(const dsa_batch* bt, const dsa_evict_inputs* in, const in
     const int64_t most = bt->max_seq_len < in->keep ? bt->max_seq_len : in->keep;   // rows a sequence can keep
     if (in->new_max_blocks < 1 || in->new_num_blocks < 1 || (int64_t)in->new_max_blocks * kPage < most) return DSA_ERR_INVALID_ARG;
     if (in->new_weight && in->new_weight_stride < most) return DSA_ERR_INVALID_ARG;
-    if (in->new_weight == in->weight) return DSA_ERR_INVALID_ARG;
+    if (in->new_weight) {
+        // [first row .. last row's end) of both: new weights are written while others are read
+        const float *w1 = in->weight + (int64_t)(bt->batch - 1) * in->weight_stride + bt->max_seq_len;
+        const float *n1 = in->new_weight + (int64_t)(bt->batch - 1) * in->new_weight_stride + most;
+        if (in->new_weight < w1 && in->weight < n1) return DSA_ERR_INVALID_ARG;
+    }
     if (in->n_arrays < 0 || (in->n_arrays > 0 && !in->arrays)) return DSA_ERR_INVALID_ARG;
     if (in->n_arrays > kEvictMaxArrays || bt->batch > 65535) return DSA_ERR_UNSUPPORTED;
     for (int i = 0; i < in->n_arrays; ++i) {
@@ -51,7 +56,7 @@ namespace {
 // CTAs per sequence of the wide kernels (0: the cluster kernel serves), and their scratch.
 int wide_ctas(const dsa_batch* bt, const DevInfo& di) {
     if (bt->max_seq_len < kEvictWide) return 0;
-    const int by_len = (bt->max_seq_len + kEvictWideRange - 1) / kEvictWideRange;
+    const int by_len = (int)(((int64_t)bt->max_seq_len + kEvictWideRange - 1) / kEvictWideRange);
     const int by_sms = di.sms / bt->batch > 8 ? di.sms / bt->batch : 8;
     return by_len < by_sms ? by_len : by_sms;
 }
@@ -90,7 +95,7 @@ dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, i
     p.B = batch->batch;
     p.max_blocks = batch->max_blocks_per_seq;
     p.num_blocks = batch->num_blocks;
-    p.max_len = batch->max_seq_len;
+    p.max_len = (int32_t)(batch->max_seq_len < kMaxLen ? batch->max_seq_len : kMaxLen);
     p.new_max_blocks = in->new_max_blocks;
     p.new_num_blocks = in->new_num_blocks;
     p.keep = in->keep;
@@ -146,7 +151,7 @@ dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, i
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, &evict_select_kernel, p)) return fail(DSA_ERR_CUDA, "eviction choice launch", e);
     }
     if (p.n_arrays == 0 && !p.new_weight) return DSA_OK;
-    const int most = batch->max_seq_len < in->keep ? batch->max_seq_len : in->keep;
+    const int64_t most = batch->max_seq_len < in->keep ? batch->max_seq_len : in->keep;
     cfg.gridDim = dim3((unsigned)((most + kEvictCopyRows - 1) / kEvictCopyRows), (unsigned)p.B, 1);
     cfg.blockDim = dim3(kEvictCopyThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;

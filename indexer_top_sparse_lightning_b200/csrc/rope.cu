@@ -39,7 +39,7 @@ dsa_status check_rope(const dsa_batch* bt, const dsa_rope_inputs* in, const void
     }
     if (in->k) {
         if (!bt->block_table || bt->max_blocks_per_seq < 1 || bt->num_blocks < 1) return DSA_ERR_INVALID_ARG;
-        if (!k_cache || !status || !aligned(in->k, 16) || !aligned(k_cache, 16)) return DSA_ERR_INVALID_ARG;
+        if (!k_cache || !status || !aligned(status, 4) || !aligned(in->k, 16) || !aligned(k_cache, 16)) return DSA_ERR_INVALID_ARG;
         if (in->k_stride_t % 8 || in->k_stride_t < 0) return DSA_ERR_INVALID_ARG;
         if (!norm_ok(in->k_norm, in->k_gamma)) return DSA_ERR_INVALID_ARG;
         if (in->kv_dtype != DSA_KV_BF16 && in->kv_dtype != DSA_KV_FP8) return DSA_ERR_INVALID_ARG;
@@ -107,14 +107,14 @@ extern "C" dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_in
         } else {
             // one token: as many of its heads as still leave eight blocks per SM (a block's
             // angles serve more rows), at least one row per slot
-            const int64_t slots = (int64_t)p.T * ((p.H + kRopeGroups - 1) / kRopeGroups);
+            const int64_t slots = (int64_t)p.T * (((int64_t)p.H + kRopeGroups - 1) / kRopeGroups);
             const int64_t rounds = slots / ((int64_t)di.sms * 8);
             p.tpc = 1;
             const int64_t hpc = (int64_t)kRopeGroups * (rounds < 1 ? 1 : rounds);
             p.hpc = hpc < p.H ? (int)hpc : p.H;
         }
-        p.hsplit = (p.H + p.hpc - 1) / p.hpc;
-        blocks = (int64_t)((p.T + p.tpc - 1) / p.tpc) * p.hsplit;
+        p.hsplit = (int)(((int64_t)p.H + p.hpc - 1) / p.hpc);
+        blocks = ((int64_t)p.T + p.tpc - 1) / p.tpc * p.hsplit;
     } else {
         p.tpc = p.hpc = p.hsplit = 1;
     }
@@ -123,7 +123,7 @@ extern "C" dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_in
     if (in->k) {
         // few tokens: one per block, so that no key waits for the angles of another
         p.ktpc = p.T <= di.sms ? 1 : tmax;
-        blocks += (p.T + p.ktpc - 1) / p.ktpc;
+        blocks += ((int64_t)p.T + p.ktpc - 1) / p.ktpc;
     } else {
         p.ktpc = 1;
     }

@@ -73,7 +73,7 @@ dsa_status plan_weight(const dsa_batch* bt, const dsa_attn_inputs* at, const Dev
 
 template <int NR>
 dsa_status launch(WeightParams& p, const WeightPlan& pl, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const DevInfo& di,
-                  int max_seq_len, cudaStream_t s) {
+                  int64_t max_seq_len, cudaStream_t s) {
     using Cfg = WeightCfg<NR>;
     const auto kernel = pl.pages ? &attn_weight_kernel<NR, true> : &attn_weight_kernel<NR, false>;
     if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kernel), Cfg::SMEM))
@@ -137,7 +137,7 @@ dsa_status dsa_attn_weight(const dsa_batch* batch, const dsa_attn_inputs* at, co
     p.max_blocks = batch->max_blocks_per_seq;
     p.num_blocks = batch->num_blocks;
     p.staged = (int32_t)pl.pages;
-    p.max_len = batch->max_seq_len;
+    p.max_len = (int32_t)(batch->max_seq_len < kMaxLen ? batch->max_seq_len : kMaxLen);
     p.max_tokens = batch->max_q_per_seq;
     p.lse = lse;
     p.weight = weight;

@@ -330,17 +330,19 @@ __global__ void __launch_bounds__(WeightCfg<NR>::THREADS, 1)
             if (sg.b < 0) break;
             // the rows' log-sum-exps in log2 units; a row that saw nothing (-inf) adds nothing
             float2* row = s_row + (ns & 1) * NR;
+            bool dead = false;
             if ((int)threadIdx.x < NR) {
                 float2 v = make_float2(0.0f, -INFINITY);
                 if ((int)threadIdx.x < sg.nrows) {
                     const float l = __ldg(p.lse + (int64_t)sg.row0 + threadIdx.x);
                     v.x = p.scale_log2;
                     if constexpr (F16) v.x *= __ldg(p.q_factor + (int64_t)sg.row0 + threadIdx.x);
-                    v.y = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+                    dead = l == -INFINITY;
+                    v.y = dead ? -INFINITY : -l * 1.4426950408889634f;
                 }
                 row[threadIdx.x] = v;
             }
-            named_bar_sync(1, 256);
+            const bool alive = named_bar_and(1, 256, !dead);     // (of the tile's real rows)
             for (int k = sg.k0; k < sg.k1; ++k, ++blk) {
                 const uint32_t b = blk & 1;
                 const int pos = k * Cfg::BLOCK + 128 * (int)crank + L;
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(WeightCfg<NR>::THREADS, 1)
                 float sum = 0.0f;
                 if (got) {
                     tc_fence_after();
-                    const bool all = __all_sync(0xffffffffu, first == 0) && sg.nrows == NR;
+                    const bool all = __all_sync(0xffffffffu, first == 0) && sg.nrows == NR && alive;
                     float a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
 #pragma unroll 1
                     for (int c0 = COLS * part; c0 < COLS * (part + 1); c0 += 32) {
@@ -376,11 +378,12 @@ __global__ void __launch_bounds__(WeightCfg<NR>::THREADS, 1)
                             e[2] = fast_exp2(fmaf(__uint_as_float(x[i + 2]), v.x * f, v.y));
                             e[3] = fast_exp2(fmaf(__uint_as_float(x[i + 3]), v.z * f, v.w));
                             if (!all) {
-                                // rows of other sequences and rows in front of the position: whatever the
-                                // scores are there, they are not added
+                                // rows of other sequences, rows in front of the position and rows that saw
+                                // nothing: whatever the scores are there, they are not added
+                                const float off[4] = {u.y, u.w, v.y, v.w};
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    if (c0 + i + j < first || c0 + i + j >= sg.nrows) e[j] = 0.0f;
+                                    if (c0 + i + j < first || off[j] == -INFINITY) e[j] = 0.0f;
                             }
                             a0 += e[0];
                             a1 += e[1];

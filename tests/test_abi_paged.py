@@ -155,3 +155,23 @@ def test_python_entry_points_want_cuda_tensors():
         dsa.dsa_cache_evict(b, torch.zeros(1, 1), 1, t.view(1, 1), [], [])
     with pytest.raises(TypeError):
         dsa.dsa_chunk_attn(b, None, kv, 0.04)
+
+
+def test_evict_rejects_new_weights_inside_the_old(lib):
+    base = 1 << 20
+    near = dict(weight=base, weight_stride=64, new_weight_stride=32)
+    assert _call_evict(lib, new_weight=base + 4 * 63, **near) == INVALID
+    assert _call_evict(lib, new_weight=base - 4 * 31, **near) == INVALID
+
+
+def test_cache_evict_rejects_counts_that_32_bits_would_wrap():
+    import torch
+    w, t = torch.zeros(1, 64), torch.zeros(1, 1, dtype=torch.int32)
+    b = dsa.Batch(t.view(1), torch.zeros(2, dtype=torch.int32), t, 1, 64, 1)
+    for kw in (dict(keep=32, sink=2 ** 32), dict(keep=32, recent=2 ** 32), dict(keep=-1)):
+        with pytest.raises(ValueError):
+            dsa.dsa_cache_evict(b, w, kw.pop("keep"), t, [], [], **kw)
+
+
+def test_rope_rejects_an_unaligned_status(lib):
+    assert _call_rope(lib, status=2) == INVALID

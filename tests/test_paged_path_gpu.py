@@ -134,3 +134,31 @@ def test_a_decode_step_captured_in_a_graph():
         want = step()
         assert_status_ok()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(w, weight)
+
+
+def test_a_fresh_workspace_is_made_on_the_call_s_stream():
+    # its zeros must be there before the kernels look at the area, whatever stream they run on
+    pg = Paged([200], [1], seed=3)
+    q, kv = randn(1, pg.T, 16, ROW).cuda(), randn(2, pg.num_blocks, PAGE, ROW).cuda()
+    torch.cuda.synchronize()
+    side, ws = torch.cuda.Stream(), dsa.Workspace(torch.device("cuda"))
+    made = []
+    get = ws.get
+    ws.get = lambda n: (made.append(torch.cuda.current_stream()), get(n))[1]
+    dsa.dsa_chunk_attn(pg.batch(), q, kv, 0.05, workspace=ws, stream=side)
+    torch.cuda.synchronize()
+    assert made[0] == side and dsa.get_status(ws) == 0
+
+
+def test_a_capture_does_not_make_the_status_area(monkeypatch):
+    monkeypatch.setattr(dsa, "_status_ws", {})
+    pg = Paged([200], [1], seed=3)
+    q, kv = randn(1, pg.T, 16, ROW).cuda(), randn(2, pg.num_blocks, PAGE, ROW).cuda()
+    b, g = pg.batch(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError, match="status_workspace"):
+            dsa.dsa_chunk_attn(b, q, kv, 0.05)
+        q.add_(0)
+    dsa.status_workspace()
+    dsa.dsa_chunk_attn(b, q, kv, 0.05)
+    assert_status_ok()

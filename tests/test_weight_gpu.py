@@ -209,3 +209,18 @@ def test_repeats_streams_and_captures_agree():
             g.replay()
     assert_status_ok()
     assert all(torch.equal(w, ref) for w in ws)
+
+
+@pytest.mark.parametrize("nq,H", [([1, 1], 128), ([1, 2], 33), ([40, 3], 64)])
+def test_rows_that_saw_nothing_add_nothing(nq, H):
+    # whatever their queries hold
+    pg = Paged([700, 300], nq, seed=5)
+    q, kv = randn(21, pg.T, H, ROW, scale=3.0).cuda(), latent(pg, 22).cuda()
+    _, lse = dsa.dsa_chunk_attn(pg.batch(), q, kv, SCALE)
+    dead = torch.rand(pg.T, H, generator=torch.Generator().manual_seed(6)).cuda() < 0.3
+    lse[dead] = -math.inf
+    clean, dirty = q.clone(), q.clone()
+    clean[dead], dirty[dead] = 0.0, math.nan
+    a, b = (dsa.dsa_attn_weight(pg.batch(), x, kv, SCALE, lse, torch.zeros(2, 700, device="cuda")) for x in (clean, dirty))
+    assert_status_ok()
+    assert torch.equal(a, b) and float(a.sum()) > 0
