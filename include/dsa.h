@@ -410,11 +410,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  *     S[t,h,s] = sm_scale * q[t,h,:] . row_s[0:576]     for s = 0..p_t
  *     out[t,h,:] = sum_s softmax(S[t,h,:])_s row_s[0:512]
  *     lse[t,h] = log sum_s exp(S[t,h,s])
- * q, cache formats and block tables are those of sparse_mla_attn; an FP8 cache
- * is dequantized once per call into the scratch (two fp16 values per element
- * and a power-of-two factor per page; the scores take both, to 2^-22 of a value,
- * the output the first, to 2^-11), which then holds max_seq_len rows of 2304
- * bytes for each sequence.
+ * q, cache formats and block tables are those of sparse_mla_attn.  Over an FP8
+ * cache the scores are fp32 sums of the codes' products, times the scales (the 64
+ * RoPE elements take part as values of 22 bits in units of their neighbours'
+ * scale), and the output's values are rounded to fp16.
  * out device [T, H, 512] bf16; lse device [T, H] fp32 (natural log) or NULL.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * bf16 (fp16 over an FP8 cache) for the second product.
@@ -452,7 +451,10 @@ DSA_API dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs*
  * s >= seq_lens[b], and all of a sequence without new tokens, are left as they
  * were.  decay >= 0, finite; with 0 the old weights are not read.
  * q, cache formats, block tables, status and the bounds reported there are those
- * of dsa_chunk_attn; positions of a page whose id is out of range add nothing.
+ * of dsa_chunk_attn; positions of a page whose id is out of range add nothing.  An
+ * FP8 cache is copied into the scratch as fp16 (two values per element and a
+ * power-of-two factor per page: 2^-22 of a value), which then holds max_seq_len
+ * rows of 2304 bytes for each sequence.
  * More than max_q_per_seq new tokens of a sequence, or a length above max_seq_len,
  * are recorded as DSA_ERR_DEVICE_BOUNDS (the surplus is not counted).
  * scratch: dsa_weight_scratch_size bytes, 256-byte aligned, of any contents, one

@@ -15,12 +15,10 @@ using namespace dsa::host;
 
 namespace {
 
-// Scratch: [headers][partial slots of the pairs][FP8: the sequences' rows as fp16, and a
-// factor per page].
+// Scratch: [headers][partial slots of the pairs].
 struct ChunkPlan {
     int pairs = 0;
-    int64_t pages = 0;          // FP8: pages per sequence of the copy
-    size_t copy_off = 0, scale_off = 0, total = 0;
+    size_t total = 0;
 };
 
 dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevInfo& di, ChunkPlan& pl) {
@@ -38,14 +36,7 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
                           (bt->batch < bt->num_tokens ? bt->batch : bt->num_tokens);
     const int64_t blocks = tiles * (((int64_t)bt->max_seq_len + ChunkCfg::BLOCK - 1) / ChunkCfg::BLOCK);
     pl.pairs = (int)(blocks < pmax ? blocks : pmax);
-    pl.copy_off = align256(ChunkCfg::HEAD_BYTES + (size_t)pmax * 4 * (size_t)ChunkCfg::PART_BYTES);
-    pl.total = pl.copy_off;
-    if (at->kv_dtype == DSA_KV_FP8) {
-        pl.pages = ((int64_t)bt->max_seq_len + kPage - 1) / kPage;
-        if (pl.pages * bt->batch > INT32_MAX / kPage) return DSA_ERR_UNSUPPORTED;   // rows of the copy, in 32 bits
-        pl.scale_off = pl.copy_off + (size_t)pl.pages * bt->batch * kPage * kCopyRow * 2;
-        pl.total = align256(pl.scale_off + (size_t)pl.pages * bt->batch * 4);
-    }
+    pl.total = align256(ChunkCfg::HEAD_BYTES + (size_t)pmax * 4 * (size_t)ChunkCfg::PART_BYTES);
     return DSA_OK;
 }
 
@@ -80,28 +71,31 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     p.H = at->H;
     p.max_blocks = batch->max_blocks_per_seq;
     p.num_blocks = batch->num_blocks;
-    p.staged = (int32_t)pl.pages;
-    const int64_t room = (pl.pages ? pl.pages : (int64_t)batch->max_blocks_per_seq) * kPage;
+    const int64_t room = (int64_t)batch->max_blocks_per_seq * kPage;
     p.max_len = (int32_t)(room < kMaxLen ? room : kMaxLen);
     p.tokens = p.max_tokens = INT32_MAX;
     p.scale_log2 = at->sm_scale * 1.4426950408889634f;
-    const void* rows = at->kv_cache;
-    uint64_t nrows = (uint64_t)batch->num_blocks * kPage;
-    if (pl.pages) {
-        void* copy = p.part + pl.copy_off;
-        float* factors = reinterpret_cast<float*>(p.part + pl.scale_off);
-        if (dsa_status st = copy_fp8_pages(batch, at, pl.pages, copy, factors, s)) return st;
-        p.page_scale = factors;
-        rows = copy;
-        nrows = (uint64_t)pl.pages * batch->batch * kPage;
+    const bool fp8 = at->kv_dtype == DSA_KV_FP8;
+    CUtensorMap tm_q, tm_k, tm_v, tm_r;
+    bool maps = rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, kDqk, 64, ChunkCfg::KCH);
+    if (fp8) {
+        p.codes = static_cast<const uint8_t*>(at->kv_cache);
+        p.kv_scale = at->kv_scale;
+        const uint64_t dims[2] = {(uint64_t)kDqk, (uint64_t)batch->num_blocks * kPage}, stride = kDqk;
+        const uint32_t bk[2] = {128, 64}, br[2] = {64, 64}, bv[2] = {256, 32};
+        auto code_map = [&](CUtensorMap* t, const uint32_t* box) {
+            return make_map(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, at->kv_cache, dims, &stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+        };
+        maps = maps && code_map(&tm_k, bk) && code_map(&tm_r, br) && code_map(&tm_v, bv);
+    } else {
+        const uint64_t nrows = (uint64_t)batch->num_blocks * kPage;
+        maps = maps && rows_map(&tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->kv_cache, nrows, kDqk, 64, 3) &&
+               rows_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->kv_cache, nrows, kDqk, 32, 4);
     }
-    CUtensorMap tm_q, tm_k, tm_v;
-    const CUtensorMapDataType kt = pl.pages ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const uint64_t row = pl.pages ? kCopyRow : kDqk;
-    if (!rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, kDqk, 64, ChunkCfg::KCH) ||
-        !rows_map(&tm_k, kt, rows, nrows, row, 64, 3) || !rows_map(&tm_v, kt, rows, nrows, row, 32, 4))
+    if (!fp8) tm_r = tm_k;         // not used
+    if (!maps)
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");
-    const auto kernel = pl.pages ? &chunk_attn_kernel<true> : &chunk_attn_kernel<false>;
+    const auto kernel = fp8 ? &chunk_attn_kernel<true> : &chunk_attn_kernel<false>;
     if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kernel), ChunkCfg::SMEM))
         return fail(DSA_ERR_CUDA, "shared memory attribute", e);
     cudaLaunchAttribute attr[2];
@@ -114,12 +108,12 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(2 * pl.pairs, 1, 1);
-    cfg.blockDim = dim3(ChunkCfg::THREADS, 1, 1);
+    cfg.blockDim = dim3(32 * ChunkCfg::warps(fp8), 1, 1);
     cfg.dynamicSmemBytes = ChunkCfg::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, tm_q, tm_k, tm_v))
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, tm_q, tm_k, tm_v, tm_r))
         return fail(DSA_ERR_CUDA, "attention launch", e);
     if (pl.pairs < 2) return DSA_OK;
     cudaLaunchConfig_t ccfg;

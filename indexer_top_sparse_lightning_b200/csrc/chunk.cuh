@@ -16,7 +16,7 @@
 // chunk_combine_kernel.
 //
 // Per block the pair runs two-CTA tensor-core MMAs (tcgen05 cta_group::2,
-// issued by one thread of CTA 0):
+// issued by CTA 0):
 //   S = Q.K^T: M = 128 rows (64 per CTA), N = 128 positions (CTA c holds page
 //       2k + c), nine K-chunks of 64 columns;
 //   O += P.V: M = 128 rows, N = 256 value columns twice (CTA c holds columns
@@ -47,7 +47,7 @@
 // tokens that see one have a non-finite score already).  Only the slots at the
 // tile's causal edge take this path (the "fixer" warp).
 //
-// Roles per CTA (448 threads):
+// Roles per CTA (448 threads; over an FP8 cache 768):
 //   warps 0-7   softmax and epilogue (warps w and w + 4 share TMEM lanes 32(w%4)..;
 //               lane L: row 64c + L%64, positions 64*(L/64).. of a block)
 //   warp 8      TMEM allocation; CTA 0: issues the score MMAs
@@ -55,135 +55,40 @@
 //   warps 10, 11  loads of keys, of values
 //   warp 12     segments (runs of one tile's blocks) and the loads of Q
 //   warp 13     fixer
+// Over an FP8 cache (chunk_fp8.cuh): warp 10 segments and Q, 11 and 12 loads of the codes of
+// keys, of values, 13 and 14 position factors, 16-19 conversion of keys, 20-23 of values.
 #pragma once
-#include "common.h"
-#include "pair.cuh"
-#include "ptx.cuh"
-#include "tiles.cuh"
+#include "chunk_cfg.cuh"
+#include "chunk_fp8.cuh"
 
 namespace dsa {
 
-struct ChunkCfg {
-    static constexpr int ROWS = 128;                    // (token, head) rows of a tile
-    static constexpr int BLOCK = 128;                   // positions of a block (two pages)
-    static constexpr int KCH = 9;                       // 64-column chunks of a latent row
-    static constexpr int KRING = 3;                     // groups of keys (64 rows x 3 chunks) that are kept
-    static constexpr int kgroups(bool f16) { return f16 ? 6 : 3; }   // groups that make a block
-    static constexpr int KGROUP = 3 * 8192;
-    static constexpr int VGROUPS = 4;                   // groups of a block's values: 32 rows x 4 chunks (this CTA's)
-    static constexpr int VRING = 3;                     // groups that are kept
-    static constexpr int VGROUP = 4 * 4096;
-    static constexpr int Q_BYTES = KCH * 64 * 128;      // this CTA's 64 rows
-    static constexpr int P_BYTES = 64 * BLOCK * 2;      // [64 rows x 128 positions] bf16: two 64-position chunks
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_P = OFF_Q + Q_BYTES;
-    static constexpr int OFF_K = OFF_P + 2 * P_BYTES;
-    static constexpr int OFF_V = OFF_K + KRING * KGROUP;
-    static constexpr int OFF_XM = OFF_V + VRING * VGROUP;   // exchange between the threads of a row
-    static constexpr int OFF_MISC = OFF_XM + 256 * 4;
-    static constexpr int MISC_BYTES = 1024;
-    static constexpr int SMEM = 1024 + OFF_MISC + MISC_BYTES;
-    static constexpr int SOFTMAX_WARPS = 8;
-    static constexpr int QK_WARP = 8, PV_WARP = 9, KEY_WARP = 10, VALUE_WARP = 11, SEG_WARP = 12, FIX_WARP = 13;
-    static constexpr int THREADS = 448;
-    // A row's reference (a maximum minus DROP) is replaced once a score exceeds it by more than LAZY.
-    // bf16 weights and fp32 sums are floating point, so a reference below the maximum costs no
-    // precision, and 2^32 (2^52 for the sums of a million weights) is far from fp32's range; a
-    // replacement waits for the P.V in flight.  fp16 weights end at 2^16 and lose bits below
-    // 2^-14: references seven below the maximum keep them in [2^-14, 2^15] down to 2^-21 of the
-    // largest weight, and to 2^-32 of it with an absolute error.
-    static constexpr float lazy(bool f16) { return f16 ? 15.0f : 32.0f; }
-    static constexpr float drop(bool f16) { return f16 ? 7.0f : 0.0f; }
-    static constexpr int NSEG = 4;                      // segment ring
-    static constexpr int TMEM_COLS = 512;               // O: [0, 256), two score buffers of 64 from column 256
-    // fp16 operands: the bf16 descriptor without its two operand-format bits
-    static constexpr uint32_t BF16_BITS = (1u << 7) | (1u << 10);
-    static constexpr uint32_t idesc_qk(bool f16) { return idesc_bf16_f32(128, BLOCK, false, false) & ~(f16 ? BF16_BITS : 0u); }
-    static constexpr uint32_t idesc_pv(bool f16) { return idesc_bf16_f32(128, 256, false, true) & ~(f16 ? BF16_BITS : 0u); }
-    // partial result of (pair, side, CTA): O [64 rows][512] fp32, then (m, sum, sum for lse, -) per row.
-    // Side 1: the pair holds the tile's first blocks; side 0: later ones.
-    static constexpr int64_t PART_O = 64 * 512 * 4;
-    static constexpr int64_t PART_BYTES = PART_O + 64 * 16;
-    static constexpr int64_t HEAD_BYTES = 2048;         // one int4 per pair: the tile that starts there and ends in a later pair
-    static constexpr int MAX_PAIRS = 128;                // the merge keeps four splits per lane
-    static constexpr int COMBINE_THREADS = 256;         // at least MAX_PAIRS
-};
-static_assert(ChunkCfg::SMEM <= 232448, "shared memory exceeds the per-CTA limit");
-static_assert(ChunkCfg::OFF_P % 1024 == 0 && ChunkCfg::OFF_K % 1024 == 0 && ChunkCfg::OFF_V % 1024 == 0, "swizzled operands need 1024-byte alignment");
-static_assert(ChunkCfg::COMBINE_THREADS >= ChunkCfg::MAX_PAIRS, "one thread per header");
-static_assert(ChunkCfg::MAX_PAIRS * 16 <= ChunkCfg::HEAD_BYTES, "one header per pair");
-
-using ChunkTiles = TileList<ChunkCfg::ROWS, ChunkCfg::BLOCK>;
-
-struct ChunkParams : ListParams {
-    uint16_t* out;            // [T, H, 512] bf16 bits
-    float* lse;               // [T, H] or null
-    uint8_t* part;            // headers, then partial results
-    uint32_t* status;         // status word; words 1-2 hold the test hooks
-    const float* page_scale;  // [B, staged] the copy's power-of-two factor of each page
-    float scale_log2;         // sm_scale * log2(e)
-};
-
-struct ChunkMisc {
-    uint64_t k_full[ChunkCfg::KRING];   // (CTA 0) the key group is ready in both CTAs
-    uint64_t k_empty[ChunkCfg::KRING];  // its MMAs have completed
-    uint64_t v_full[ChunkCfg::VRING];   // (CTA 0) the value group is ready in both CTAs
-    uint64_t v_empty[ChunkCfg::VRING];
-    uint64_t v_peer[ChunkCfg::VRING];     // (CTA 0) CTA 1's fixer is done with the group
-    uint64_t v_land[ChunkCfg::VRING];   // the group has landed, for the fixer to look at
-    uint64_t q_full;                      // (CTA 0) Q of both CTAs
-    uint64_t q_land;                      // (fp16) this CTA's Q, still bf16
-    uint64_t q_empty;
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-    uint64_t o_full, o_empty, drain[2];
-    uint64_t seg_full[ChunkCfg::NSEG], seg_empty[ChunkCfg::NSEG];
-    TileRun seg[ChunkCfg::NSEG];
-    uint64_t wait_ns;
-    ShareStart start;
-    int64_t sums[ChunkCfg::THREADS / 32];
-    uint32_t tmem_base;
-    int abort;
-    uint32_t inject;
-};
-static_assert(sizeof(ChunkMisc) <= ChunkCfg::MISC_BYTES, "misc block exceeds its slot");
-
-// The 32-position groups of a block that the value product runs over.
-struct ChunkBlock {
-    int ngroups;              // 32-position groups that some row sees (1..4)
-    int fix_from;             // first group that the fixer looks at (ngroups: none)
-};
-__device__ __forceinline__ ChunkBlock chunk_block(const TileRun& s, int k) {
-    ChunkBlock r;
-    const int left = s.see - k * ChunkCfg::BLOCK;          // positions of the block that some row sees
-    r.ngroups = left >= ChunkCfg::BLOCK ? 4 : left > 0 ? (left + 31) / 32 : 0;
-    const int all = s.see_all - k * ChunkCfg::BLOCK;       // ... that every row sees
-    r.fix_from = all <= 0 ? 0 : all / 32;
-    if (r.fix_from > r.ngroups) r.fix_from = r.ngroups;
-    return r;
-}
-
-// F16: the cache is the fp16 copy of an FP8 cache (latent.cu), and Q is
-// brought to fp16 in shared memory: both operands of an MMA have one type, and
-// bf16 would round the products of codes and scales eight times as far.  A row of
-// the copy holds the 576 rounded values and what their rounding left out; the
-// scores take both (twice the score MMAs and key loads: with the rounded values
-// alone lse was off by 6e-6 of itself, with both by 3e-7), the value product the
-// first.  Powers of two keep the values in fp16's range: one per row of Q,
-// one per page f_s of the copy.  With t_s = S_s + log2 f_s the weights that
-// multiply the copy's rows are P_s f_s = 2^(t_s - m), so the reference m follows
-// t, and the sums of weights are those of 2^(t_s - m) / f_s.
-template <bool F16>
-__global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
+// FP8: the cache holds e4m3 codes, which chunk_fp8.cuh brings to fp16 operands, and Q is
+// brought to fp16 in shared memory: both operands of an MMA have one type, and bf16
+// would round the products of codes and scales eight times as far.  A power of two per
+// row of Q keeps it in fp16's range.  The scores are put together from four accumulators
+// here; with t_s = S_s + log2 F_s (F_s the position's power of two) the weights that multiply
+// the values code * f / F are P_s F_s = 2^(t_s - m), so the reference m follows t, and the
+// sums of weights are those of 2^(t_s - m) / F_s.
+template <bool FP8>
+__global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
-                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_r) {
     using Cfg = ChunkCfg;
+    constexpr int SMW = Cfg::SOFTMAX_WARPS, QK_WARP = SMW, PV_WARP = SMW + 1;
+    constexpr int KEY_WARP = SMW + 2, VALUE_WARP = SMW + 3, FIX_WARP = SMW + 5;
+    constexpr int KLOAD_WARP = SMW + 3, VLOAD_WARP = SMW + 4, FACTOR_WARP = SMW + 5;                 // FP8 (two factor warps)
+    constexpr int FKEY_WARP = SMW + 8, FVALUE_WARP = FKEY_WARP + Cfg::CONV_WARPS;
+    constexpr int SEG_WARP = FP8 ? SMW + 2 : SMW + 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_shared(smem_raw, 1024);
     uint8_t* s_q = smem + Cfg::OFF_Q;
     uint8_t* s_p = smem + Cfg::OFF_P;
-    uint8_t* s_k = smem + Cfg::OFF_K;
-    uint8_t* s_v = smem + Cfg::OFF_V;
-    float* s_xm = reinterpret_cast<float*>(smem + Cfg::OFF_XM);
+    uint8_t* s_k = smem + (FP8 ? Cfg::OFF_FK : Cfg::OFF_K);
+    uint8_t* s_v = smem + (FP8 ? Cfg::OFF_FV : Cfg::OFF_V);
+    ChunkScales* s_rec = reinterpret_cast<ChunkScales*>(smem + Cfg::OFF_REC);
+    float* s_xm = reinterpret_cast<float*>(smem + (FP8 ? kChunkFp8Xm : Cfg::OFF_XM));
     ChunkMisc* m = reinterpret_cast<ChunkMisc*>(smem + Cfg::OFF_MISC);
     volatile int* abort = &m->abort;
 
@@ -194,43 +99,60 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < Cfg::KRING; ++i) {
-            mbar_init(&m->k_full[i], 1);    // CTA 0's loader, for both CTAs
-            mbar_init(&m->k_empty[i], 1);
+            mbar_init(&m->k_full[i], FP8 ? 2 : 1);    // CTA 0's loader, for both CTAs; FP8: both CTAs' converters
+            mbar_init(&m->k_empty[i], FP8 ? 2 : 1);
+            mbar_init(&m->kc_empty[i], 1);
         }
         for (int i = 0; i < Cfg::VRING; ++i) {
-            mbar_init(&m->v_full[i], 1);    // CTA 0's loader or fixer, for both CTAs
+            mbar_init(&m->v_full[i], FP8 ? 2 : 1);    // ... or fixer
             mbar_init(&m->v_peer[i], 1);
-            mbar_init(&m->v_empty[i], 1);
+            mbar_init(&m->v_empty[i], FP8 ? 2 : 1);
             mbar_init(&m->v_land[i], 1);
         }
-        mbar_init(&m->q_full, F16 ? 2 * Cfg::SOFTMAX_WARPS : 2);
+        mbar_init(&m->q_full, FP8 ? 2 * SMW : 2);
         mbar_init(&m->q_land, 1);
         mbar_init(&m->q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&m->s_full[i], 1);
-            mbar_init(&m->s_empty[i], 2 * Cfg::SOFTMAX_WARPS);   // those of both CTAs
-            mbar_init(&m->p_full[i], 2 * Cfg::SOFTMAX_WARPS);
+            mbar_init(&m->s_empty[i], 2 * SMW);   // those of both CTAs
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m->p_full[i], 2 * SMW);
             mbar_init(&m->p_empty[i], 1);
             mbar_init(&m->drain[i], 1);
         }
         mbar_init(&m->o_full, 1);
-        mbar_init(&m->o_empty, 2 * Cfg::SOFTMAX_WARPS);
+        mbar_init(&m->o_empty, 2 * SMW);
         for (int i = 0; i < Cfg::NSEG; ++i) {
             mbar_init(&m->seg_full[i], 1);
-            mbar_init(&m->seg_empty[i], Cfg::SOFTMAX_WARPS + (crank == 0 ? 5 : 3));   // loading and fixer warps; CTA 0: the issuers too
+            // FP8: factors and converting warps; else loading and fixer warps; CTA 0: the issuers too
+            mbar_init(&m->seg_empty[i], SMW + (FP8 ? 4 + 2 * Cfg::CONV_WARPS : 3) + (crank == 0 ? 2 : 0));
+        }
+        for (int i = 0; i < Cfg::NREC; ++i) {
+            mbar_init(&m->rec_full[i], 2);
+            mbar_init(&m->rec_empty[i], SMW + 2);
+        }
+        if (FP8) {
+            // the operand rings are empty: no MMAs to wait for in their first round
+            for (int i = 0; i < Cfg::KRING; ++i) mbar_arrive(&m->k_empty[i]);
+            for (int i = 0; i < Cfg::FVRING; ++i) {
+                mbar_init(&m->vc_empty[i], 1);
+                mbar_arrive(&m->v_empty[i]);
+            }
         }
         m->abort = 0;
         m->start.b = -1;
         fence_mbar_init();
     }
-    if (warp == Cfg::QK_WARP) {
+    if (warp == QK_WARP) {
         tmem_alloc_2cta(&m->tmem_base, Cfg::TMEM_COLS);
         tmem_relinquish_2cta();
     }
-    if (warp == Cfg::SEG_WARP && lane == 0) {
+    if (warp == SEG_WARP && lane == 0) {
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
+        if (FP8) prefetch_tmap(&tm_r);
     }
     // the merge kernel (a programmatic dependent) may be scheduled on SMs this grid
     // leaves idle; it waits for the whole grid before reading anything
@@ -248,14 +170,14 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = m->tmem_base;
     const uint32_t tm_o = tmem_base;            // columns [0, 256)
-    const uint32_t tm_s = tmem_base + 256;      // score buffers, 64 columns each
+    const uint32_t tm_s = tmem_base + 256;      // score buffers, 64 columns each (FP8: one, of four times that)
     const uint64_t wlim = m->wait_ns;
 
     // ---------------------------------------------------------------- this pair's share of the list
     int64_t g0, g1, total;
-    ChunkTiles::share<Cfg::THREADS>(p, pair, np, m->sums, &m->start, p.status, g0, g1, total);
+    ChunkTiles::share<32 * Cfg::warps(FP8)>(p, pair, np, m->sums, &m->start, p.status, g0, g1, total);
 
-    if (warp == Cfg::SEG_WARP) {
+    if (warp == SEG_WARP) {
         // ---------------------------------------------------------------- segments, loads of Q
         ChunkTiles::Walk w = ChunkTiles::begin(p, m->start, g0, g1);
         // for the merge: first row, rows and pairs of the tile that starts here and ends in a later pair
@@ -286,7 +208,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     ok = false;
                     break;
                 }
-                if constexpr (F16) {
+                if constexpr (FP8) {
                     mbar_arrive_expect_tx(&m->q_land, Cfg::Q_BYTES);
                     tma_load_3d(s_q, &tm_q, &m->q_land, 0, sg.row0 + 64 * (int)crank, 0);
                 } else {
@@ -300,13 +222,23 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             if (crank == 0) reinterpret_cast<int4*>(p.part)[pair] = head;
         }
         __syncwarp();
-    } else if (warp == Cfg::KEY_WARP || warp == Cfg::VALUE_WARP) {
+    } else if (FP8 && warp >= KLOAD_WARP) {
+        // ---------------------------------------------------------------- an FP8 cache: codes, factors, keys, values
+        const int ti = (int)threadIdx.x - 32 * (warp < FVALUE_WARP ? FKEY_WARP : FVALUE_WARP);
+        bool ok = !(crank == 1 && (m->inject & 4u));   // test hook: the second CTA never loads
+        if (ok && warp != FACTOR_WARP + 2)
+            ok = warp < FACTOR_WARP   ? fp8_codes(p, m, smem, tm_k, tm_r, tm_v, warp == KLOAD_WARP, crank, abort, wlim)
+                 : warp < FKEY_WARP   ? fp8_factors(p, m, s_rec, warp - FACTOR_WARP, crank, abort, wlim)
+                 : warp < FVALUE_WARP ? fp8_keys(p, m, smem, ti, crank, abort, wlim)
+                                      : fp8_values(p, m, smem, ti, crank, abort, wlim);
+        if (!ok) *abort = 1;
+    } else if (!FP8 && (warp == KEY_WARP || warp == VALUE_WARP)) {
         // ---------------------------------------------------------------- loads of keys, of values
         // The whole warp runs the schedule and one elected lane acts, so that addresses and
         // coordinates stay in uniform registers (per-lane values would have to be moved there for
         // every copy).  CTA 0 announces the bytes of both CTAs (both see the same page ids), so
         // that CTA 1 only issues its copies.
-        const bool keys = warp == Cfg::KEY_WARP;
+        const bool keys = warp == KEY_WARP;
         const bool el = elect_one();
         // test hook: the second CTA never loads
         bool ok = !(crank == 1 && (m->inject & 4u));
@@ -315,11 +247,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         const uint32_t k_lead = mapa_shared(smem_u32(&m->k_full[0]), 0), v_lead = mapa_shared(smem_u32(&m->v_full[0]), 0);
         TileRun sg = {};
         const int32_t* table = nullptr;
-        auto page_id = [&](int page) -> int {          // -1: nobody sees the page; -2: a bad id
-            if (page >= p.max_blocks || page * kPage >= sg.see) return -1;
-            const int id = __ldg(table + page);
-            return id >= 0 && id < p.num_blocks ? (p.staged ? sg.b * p.staged + page : id) : -2;
-        };
+        auto page_id = [&](int page) -> int { return chunk_page(p, sg, table, page); };
         auto load_keys = [&](int id0, int id1) -> bool {
             const int id = crank == 0 ? id0 : id1;
             // a page that nobody sees is not loaded: its scores are replaced whatever they are
@@ -327,15 +255,12 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             const bool mine = el && id >= 0;
             const int y = id * kPage;
 #pragma unroll 1
-            for (int g = 0; g < Cfg::kgroups(F16); ++g) {
-                const int kr = g % Cfg::KRING;
-                if (!elected_wait(el, &m->k_empty[kr], ph, abort, wlim)) return false;
-                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[kr], bytes);
-                // (fp16: the small rests first, so that adding them up costs no bits of the sum)
-                const int chunk = F16 && g < Cfg::KRING ? 3 * g + 9 : F16 ? 3 * g - 9 : 3 * g;
-                if (mine) tma_load_3d_pair(s_k + kr * Cfg::KGROUP, &tm_k, k_lead + 8 * kr, 0, y, chunk);
-                if (kr == Cfg::KRING - 1) ph ^= 1;
+            for (int g = 0; g < Cfg::KRING; ++g) {
+                if (!elected_wait(el, &m->k_empty[g], ph, abort, wlim)) return false;
+                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[g], bytes);
+                if (mine) tma_load_3d_pair(s_k + g * Cfg::KGROUP, &tm_k, k_lead + 8 * g, 0, y, 3 * g);
             }
+            ph ^= 1;
             return true;
         };
         auto next_group = [&]() {
@@ -411,7 +336,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         }
         if (bad && el) atomicCAS(p.status, 0u, (uint32_t)kStBounds);
         if (!ok) *abort = 1;
-    } else if (warp == Cfg::FIX_WARP) {
+    } else if (!FP8 && warp == FIX_WARP) {
         // ---------------------------------------------------------------- value rows at the causal edge
         bool ok = true;
         uint32_t n = 0, phase = 0, peer = 0;   // groups so far; next phase of each land and peer barrier
@@ -463,7 +388,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                     const int pos = k * Cfg::BLOCK + 32 * g + lane;
                     bool zero = pos >= sg.see;
                     if (!zero && pos >= sg.see_all) {
-                        constexpr uint32_t EXP = F16 ? 0x7C00u : 0x7F80u;
+                        constexpr uint32_t EXP = 0x7F80u;
                         uint32_t odd = 0;  // an exponent of all ones
 #pragma unroll 1
                         for (int q = 0; q < 32; ++q) {
@@ -492,13 +417,13 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             }
         }
         if (!ok) *abort = 1;
-    } else if (warp == Cfg::QK_WARP || warp == Cfg::PV_WARP) {
+    } else if (warp == QK_WARP || warp == PV_WARP) {
         // ---------------------------------------------------------------- MMA issuers (CTA 0)
         // The whole warp runs the schedule and one elected lane issues, so that the operand
         // descriptors stay in uniform registers: 30 cycles per MMA where descriptors kept per
         // lane cost 51 (the MMAs themselves take 32 and 64).  Descriptors differ from a base by
         // multiples of 16 bytes in their low words.
-        const bool qk = warp == Cfg::QK_WARP;
+        const bool qk = warp == QK_WARP;
         if (crank == 0) {
             const bool el = elect_one();
             bool ok = true;
@@ -509,34 +434,64 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             // apart (LBO), 8-row groups 1024 B (SBO)
             const uint64_t v_desc = sdesc_sw128(smem_u32(s_v), 4096, 1024);
             uint32_t blk = 0;              // blocks so far
-            uint32_t r = 0, ph = 0;        // group of the value ring; parity of the keys' or values' ring
+            uint32_t r = 0, ph = 0;        // group of the (FP8 key or) value ring; parity of the keys' or values' ring
             auto issue_qk = [&](bool last) -> bool {
-                // scores of this buffer's block before have been read
-                if (!elected_wait(el, &m->s_empty[blk & 1], ((blk >> 1) & 1) ^ 1, abort, wlim)) return false;
-                tc_fence_after();
-                const uint32_t d = tm_s + (blk & 1) * 64;
+                if constexpr (FP8) {
+                    // the fifth tile in two parts, both times Q's last chunk, and tile 3 into the last
+                    // accumulator; tiles 0 to 2 into their own
 #pragma unroll 1
-                for (int g = 0; g < Cfg::kgroups(F16); ++g) {
-                    const int kr = g % Cfg::KRING;
-                    if (!elected_wait(el, &m->k_full[kr], ph, abort, wlim)) return false;
-                    const uint32_t base = kr * (Cfg::KGROUP / 16);   // of Q's chunks as well: 8192 bytes each
-#pragma unroll
-                    for (int j = 0; j < 12; ++j)
-                        if (el) {
-                            const uint32_t off = base + (j >> 2) * 512 + (j & 3) * 2;
-                            umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::idesc_qk(F16), (g | j) != 0);
+                    for (int g = 0; g < 5; ++g) {
+                        const int tile = g < 2 ? 3 : g - 2;
+                        // this accumulator's scores of the block before have been read
+                        if (g != 1) {
+                            if (!elected_wait(el, &m->s_empty[tile], (blk & 1) ^ 1, abort, wlim)) return false;
+                            tc_fence_after();
                         }
-                    if (el) umma_commit_2cta(&m->k_empty[kr], 3);
-                    if (kr == Cfg::KRING - 1) ph ^= 1;
+                        if (!elected_wait(el, &m->k_full[r], ph, abort, wlim)) return false;
+                        const uint32_t d = tm_s + 64 * tile;
+                        const uint64_t kd = k_desc + r * (Cfg::FGROUP / 16);
+                        const uint64_t qd = q_desc + (g == 0 ? 8 : 2 * tile) * 512;
+                        const uint32_t step = g == 0 ? 0 : 512;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (el)
+                                umma_bf16_2cta(d, qd + ((j >> 2) * step + (j & 3) * 2), kd + ((j >> 2) * 512 + (j & 3) * 2),
+                                               Cfg::idesc_qk(FP8), j != 0 || g == 1);
+                        if (el) umma_commit_2cta(&m->k_empty[r], 3);
+                        if (el && g > 0) umma_commit_2cta(&m->s_full[tile], 3);
+                        if (++r == Cfg::KRING) {
+                            r = 0;
+                            ph ^= 1;
+                        }
+                    }
+                } else {
+                    // scores of this buffer's block before have been read
+                    if (!elected_wait(el, &m->s_empty[blk & 1], ((blk >> 1) & 1) ^ 1, abort, wlim)) return false;
+                    tc_fence_after();
+                    const uint32_t d = tm_s + (blk & 1) * 64;
+#pragma unroll 1
+                    for (int g = 0; g < Cfg::KRING; ++g) {
+                        if (!elected_wait(el, &m->k_full[g], ph, abort, wlim)) return false;
+                        const uint32_t base = g * (Cfg::KGROUP / 16);   // of Q's chunks as well: 8192 bytes each
+#pragma unroll
+                        for (int j = 0; j < 12; ++j)
+                            if (el) {
+                                const uint32_t off = base + (j >> 2) * 512 + (j & 3) * 2;
+                                umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::idesc_qk(FP8), (g | j) != 0);
+                            }
+                        if (el) umma_commit_2cta(&m->k_empty[g], 3);
+                    }
+                    ph ^= 1;
+                    if (el) umma_commit_2cta(&m->s_full[blk & 1], 3);
                 }
-                if (el) umma_commit_2cta(&m->s_full[blk & 1], 3);
                 if (last && el) umma_commit_2cta(&m->q_empty, 3);
                 return true;
             };
             auto issue_pv = [&](int ngroups, bool first, bool last) -> bool {
-                if (!elected_wait(el, &m->p_full[blk & 1], (blk >> 1) & 1, abort, wlim)) return false;
+                const uint32_t pb = FP8 ? 0u : blk & 1;
+                if (!elected_wait(el, &m->p_full[pb], (FP8 ? blk : blk >> 1) & 1, abort, wlim)) return false;
                 tc_fence_after();
-                const uint64_t pd = p_desc + (blk & 1) * (Cfg::P_BYTES / 16);
+                const uint64_t pd = p_desc + pb * (Cfg::P_BYTES / 16);
 #pragma unroll 1
                 for (int g = 0; g < ngroups; ++g) {
                     if (!elected_wait(el, &m->v_full[r], ph, abort, wlim)) return false;
@@ -547,14 +502,14 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                         for (int s16 = 0; s16 < 2; ++s16)
                             if (el)        // A = P [64 rows x 16 positions] K-major
                                 umma_bf16_2cta(tm_o + h * 128, pd + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
-                                               vd + (h * 512 + s16 * 128), Cfg::idesc_pv(F16), g > 0 || s16 > 0 || !first);
+                                               vd + (h * 512 + s16 * 128), Cfg::idesc_pv(FP8), g > 0 || s16 > 0 || !first);
                     if (el) umma_commit_2cta(&m->v_empty[r], 3);
-                    if (++r == Cfg::VRING) {
+                    if (++r == (FP8 ? Cfg::FVRING : Cfg::VRING)) {
                         r = 0;
                         ph ^= 1;
                     }
                 }
-                if (el) umma_commit_2cta(&m->p_empty[blk & 1], 3);
+                if (el) umma_commit_2cta(&m->p_empty[pb], 3);
                 if (last && el) umma_commit_2cta(&m->o_full, 3);
                 return true;
             };
@@ -587,35 +542,42 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax + epilogue
-        // Four threads share a row: positions 64 * half + 32 * part .. of a block each, and 128
-        // value columns each in the end.
+        // 2 * PARTS threads share a row: NP positions of a block each, and VC value columns each in
+        // the end.
+        constexpr int PARTS = SMW / 4, SMT = 32 * SMW, NP = 64 / PARTS, VC = 256 / PARTS;
         const int L = threadIdx.x & 127;             // TMEM lane
         const int part = threadIdx.x >> 7;
         const int hl = L & 63;                       // row of this CTA's 64
         const int half = L >> 6;
         const int rr = 64 * (int)crank + hl;         // row of the tile
-        const int p0 = 64 * half + 32 * part;        // first position of this thread in a block
+        const int p0 = 64 * half + NP * part;        // first position of this thread in a block
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tm_mine = tm_o + lane_off + 128 * part;
-        const int col0 = 256 * half + 128 * part;    // first of this thread's value columns
-        // the row's value of all four threads combined; `x` of every thread is out before any is read
-        auto exchange = [&](float x, float (&of)[4]) {
+        const uint32_t tm_mine = tm_o + lane_off + VC * part;
+        const int col0 = 256 * half + VC * part;     // first of this thread's value columns
+        // the row's values of all its threads; `x` of every thread is out before any is read
+        auto exchange = [&](float x, float (&of)[2 * PARTS]) {
             s_xm[128 * part + L] = x;
-            named_bar_sync(1, 256);
-            of[0] = s_xm[hl];
-            of[1] = s_xm[hl + 64];
-            of[2] = s_xm[hl + 128];
-            of[3] = s_xm[hl + 192];
-            named_bar_sync(1, 256);
+            named_bar_sync(1, SMT);
+#pragma unroll
+            for (int i = 0; i < 2 * PARTS; ++i) of[i] = s_xm[hl + 64 * i];
+            named_bar_sync(1, SMT);
+        };
+        auto row_sum = [&](float x) -> float {
+            float of[2 * PARTS];
+            exchange(x, of);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * PARTS; i += 2) sum += of[i] + of[i + 1];
+            return sum;
         };
         uint32_t blk = 0;
         bool ok = true;
-        // Every exit decision of these 256 threads is taken together (votes carried
+        // Every exit decision of these threads is taken together (votes carried
         // by named barriers), so the named barriers always match.
         for (int ns = 0;; ++ns) {
             const int sr = ns % Cfg::NSEG;
             const bool there = warp_wait(&m->seg_full[sr], (ns / Cfg::NSEG) & 1, abort, wlim);
-            ok = named_bar_and(1, 256, ok && there);
+            ok = named_bar_and(1, SMT, ok && there);
             if (!ok) break;
             const TileRun sg = m->seg[sr];
             __syncwarp();
@@ -627,29 +589,23 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             // computed and dropped)
             const int see = real ? sg.c + tok + 1 : sg.see;
             const int32_t* table = p.block_table + (int64_t)sg.b * p.max_blocks;
-            auto page_ok = [&](int k) -> bool {
-                const int page = 2 * k + half;
-                if (page >= p.max_blocks || page * kPage >= sg.see) return true;   // masked by position
-                const int id = __ldg(table + page);
-                return id >= 0 && id < p.num_blocks;
-            };
+            auto page_ok = [&](int k) -> bool { return FP8 || chunk_page(p, sg, table, 2 * k + half) != -2; };
             float c_row = p.scale_log2;                  // scores in log2 units
-            const float* page_scale = nullptr;
-            if constexpr (F16) {
-                page_scale = p.page_scale + (int64_t)sg.b * p.staged;
+            if constexpr (FP8) {
                 ok = warp_wait(&m->q_land, ns & 1, abort, wlim);
-                ok = named_bar_and(1, 256, ok);
+                ok = named_bar_and(1, SMT, ok);
                 if (!ok) break;
-                // This row's 72 pieces of 16 bytes, 18 for each of its threads (in an order that spreads
+                // This row's 72 pieces of 16 bytes, shared out over its threads (in an order that spreads
                 // the lanes over the banks): the largest magnitude, then fp16 of value * 2^(13 - E).
-                const int quarter = 2 * part + half;
+                constexpr int PIECES = 36 / PARTS;
+                const int share = 2 * part + half;
                 auto piece = [&](int i) -> uint4* {
-                    const int j = 18 * quarter + i;
+                    const int j = PIECES * share + i;
                     return reinterpret_cast<uint4*>(s_q + (j >> 3) * 8192 + hl * 128 + (((j + hl) & 7) << 4));
                 };
                 uint32_t top = 0;                        // bf16 magnitudes compare as integers
 #pragma unroll 1
-                for (int i = 0; i < 18; ++i) {
+                for (int i = 0; i < PIECES; ++i) {
                     const uint4 v = *piece(i);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -658,15 +614,16 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                         top = max(top, (w[e] >> 16) & 0x7FFFu);
                     }
                 }
-                float of[4];
+                float of[2 * PARTS];
                 exchange(__uint_as_float(top << 16), of);    // (NaN: above infinity as an integer)
-                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(of[e]) >> 16);
+#pragma unroll
+                for (int e = 0; e < 2 * PARTS; ++e) top = max(top, __float_as_uint(of[e]) >> 16);
                 int E = (int)(top >> 7) - 127;
                 E = E < -100 ? -100 : E > 127 ? 127 : E;
                 const float down = __uint_as_float((uint32_t)(13 - E + 127) << 23);
                 c_row *= __uint_as_float((uint32_t)(E - 13 + 127) << 23);
 #pragma unroll 1
-                for (int i = 0; i < 18; ++i) {
+                for (int i = 0; i < PIECES; ++i) {
                     const uint4 v = *piece(i);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     uint32_t o[4];
@@ -683,77 +640,120 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 if (lane == 0) arrive_leader(&m->q_full, crank);
             }
             bool next_ok = page_ok(sg.k0);
-            float next_f = 1.0f;
-            if constexpr (F16)
-                if ((2 * sg.k0 + half) * kPage < sg.see) next_f = __ldg(page_scale + 2 * sg.k0 + half);
             float mrun = -INFINITY, lrun = 0.0f, lfull = 0.0f;
             for (int k = sg.k0; k < sg.k1; ++k, ++blk) {
-                const uint32_t b = blk & 1, u = (blk >> 1) & 1;
-                const bool this_ok = next_ok;
-                const float fk = next_f;
-                if (k + 1 < sg.k1) {
-                    next_ok = page_ok(k + 1);
-                    if constexpr (F16)
-                        if ((2 * (k + 1) + half) * kPage < sg.see) next_f = __ldg(page_scale + 2 * (k + 1) + half);
-                }
-                const bool got = ok && warp_wait(&m->s_full[b], u, abort, wlim);
-                float sv[32];
+                const uint32_t b = FP8 ? 0u : blk & 1, u = (FP8 ? blk : blk >> 1) & 1;
+                bool this_ok = next_ok;
+                const ChunkScales& rec = s_rec[blk % Cfg::NREC];
+                if (k + 1 < sg.k1) next_ok = page_ok(k + 1);
+                bool got = ok && (FP8 ? warp_wait(&m->rec_full[blk % Cfg::NREC], (blk / Cfg::NREC) & 1, abort, wlim)
+                                      : warp_wait(&m->s_full[b], u, abort, wlim));
+                float2 sv[NP / 2];
                 float mx = -INFINITY;
+                if constexpr (FP8) {
+                    // the accumulators in the order in which they are made: 3, 0, 1, 2
+                    this_ok = rec.ok[half] != 0;
+#pragma unroll
+                    for (int i = 0; i < NP / 2; ++i) sv[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+                    for (int i4 = 0; got && i4 < 4; ++i4) {
+                        const int t = (i4 + 3) & 3;
+                        got = warp_wait(&m->s_full[t], blk & 1, abort, wlim);
+                        if (got) {
+                            uint32_t a[NP];
+                            tc_fence_after();
+                            tmem_ld32(tm_s + lane_off + 64 * t + NP * part, a);
+                            tmem_wait_ld();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_leader(&m->s_empty[t], crank);
+                            const float4* f4 = reinterpret_cast<const float4*>(&rec.f[t][p0]);
+#pragma unroll
+                            for (int i = 0; i < NP; i += 4) {
+                                const float4 f = f4[i / 4];
+                                sv[i / 2] = fma_f32x2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])),
+                                                      make_float2(f.x, f.y), sv[i / 2]);
+                                sv[i / 2 + 1] = fma_f32x2(make_float2(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])),
+                                                          make_float2(f.z, f.w), sv[i / 2 + 1]);
+                            }
+                        }
+                    }
+                }
                 if (got) {
-                    tc_fence_after();
-                    uint32_t a[32];
-                    tmem_ld32(tm_s + lane_off + b * 64 + 32 * part, a);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_leader(&m->s_empty[b], crank);
+                    if constexpr (!FP8) {
+                        tc_fence_after();
+                        uint32_t a[NP];
+                        tmem_ld32(tm_s + lane_off + b * 64 + NP * part, a);
+                        tmem_wait_ld();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_leader(&m->s_empty[b], crank);
+#pragma unroll
+                        for (int i = 0; i < NP; i += 2)
+                            sv[i / 2] = mul_f32x2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), make_float2(c_row, c_row));
+                    } else {
+                        const float4* l4 = reinterpret_cast<const float4*>(&rec.log2f[p0]);
+#pragma unroll
+                        for (int i = 0; i < NP; i += 4) {
+                            const float4 l = l4[i / 4];
+                            sv[i / 2] = fma_f32x2(sv[i / 2], make_float2(c_row, c_row), make_float2(l.x, l.y));
+                            sv[i / 2 + 1] = fma_f32x2(sv[i / 2 + 1], make_float2(c_row, c_row), make_float2(l.z, l.w));
+                        }
+                    }
                     // positions of this thread that the row sees
                     const int vis = this_ok ? see - (k * Cfg::BLOCK + p0) : 0;
+                    if (!__all_sync(0xffffffffu, vis >= NP))
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        sv[i] = F16 ? fmaf(__uint_as_float(a[i]), c_row * fk, log2_of_power(fk)) : __uint_as_float(a[i]) * c_row;
-                    if (!__all_sync(0xffffffffu, vis >= 32))
+                        for (int i = 0; i < NP; i += 2) {
+                            sv[i / 2].x = i < vis ? sv[i / 2].x : -INFINITY;
+                            sv[i / 2].y = i + 1 < vis ? sv[i / 2].y : -INFINITY;
+                        }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sv[i] = i < vis ? sv[i] : -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, sv[i]);
+                    for (int i = 0; i < NP / 2; ++i) mx = fmaxf(mx, fmaxf(sv[i].x, sv[i].y));
                 }
                 // The reference maximum stays while no thread's scores are above it by more than the limit
                 // (one barrier, no exchange); otherwise every row takes its new maximum.
                 float muse = mrun;
                 bool rescale = false;
-                if (!named_bar_and(1, 256, ok && got && !(mx > mrun + Cfg::lazy(F16)))) {
-                    ok = named_bar_and(1, 256, ok && got);
+                if (!named_bar_and(1, SMT, ok && got && !(mx > mrun + Cfg::lazy(FP8)))) {
+                    ok = named_bar_and(1, SMT, ok && got);
                     if (!ok) break;
-                    float of[4];
+                    float of[2 * PARTS], mnew = -INFINITY;
                     exchange(mx, of);
-                    const float mnew = fmaxf(fmaxf(of[0], of[1]), fmaxf(of[2], of[3]));
-                    rescale = mnew > mrun + Cfg::lazy(F16);      // identical in the four threads of a row
-                    if (rescale) muse = mnew - Cfg::drop(F16);
+#pragma unroll
+                    for (int i = 0; i < 2 * PARTS; ++i) mnew = fmaxf(mnew, of[i]);
+                    rescale = mnew > mrun + Cfg::lazy(FP8);      // identical in the threads of a row
+                    if (rescale) muse = mnew - Cfg::drop(FP8);
                 }
                 const float base = muse == -INFINITY ? 0.0f : muse;   // (nothing seen yet: 2^-inf)
-                uint32_t pk[16];
-                float r0 = 0.0f, r1 = 0.0f, f0 = 0.0f, f1 = 0.0f;
+                uint32_t pk[NP / 2];
+                float2 rounded = make_float2(0.0f, 0.0f), full = rounded;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float e0 = fast_exp2(sv[2 * i] - base);
-                    const float e1 = fast_exp2(sv[2 * i + 1] - base);
+                for (int i = 0; i < NP / 2; ++i) {
+                    const float2 x = add_f32x2(sv[i], make_float2(-base, -base));
+                    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                     // O is divided by the sum of the rounded weights that the MMA multiplies (their
                     // roundings cancel in part); lse takes the sum before rounding.  fp16 weights
-                    // divide by that one as well: divided by a small page factor, the rounding of a
+                    // divide by that one as well: divided by a small F, the rounding of a
                     // weight that is subnormal in fp16 would count in the sum as it does not in O.
-                    if constexpr (F16) {
-                        const __half2 h = __floats2half2_rn(e0, e1);
+                    if constexpr (FP8) {
+                        const __half2 h = __floats2half2_rn(e.x, e.y);
                         pk[i] = *reinterpret_cast<const uint32_t*>(&h);
                     } else {
-                        pk[i] = pack_bf16(e0, e1);
-                        r0 += __uint_as_float(pk[i] << 16);
-                        r1 += __uint_as_float(pk[i] & 0xFFFF0000u);
+                        pk[i] = pack_bf16(e.x, e.y);
+                        rounded = add_f32x2(rounded, make_float2(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
                     }
-                    f0 += e0;
-                    f1 += e1;
+                    if constexpr (FP8) {
+                        full = fma_f32x2(e, reinterpret_cast<const float2*>(&rec.inv[p0])[i], full);
+                    } else {
+                        full = add_f32x2(full, e);
+                    }
                 }
-                // weight buffer b is free once P.V of block blk - 2 completed
+                if constexpr (FP8) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m->rec_empty[blk % Cfg::NREC]);
+                }
+                // weight buffer b is free once P.V of block blk - 2 (FP8: blk - 1) completed
                 ok = warp_wait(&m->p_empty[b], u ^ 1, abort, wlim);
                 float f = 1.0f;
                 const bool need = rescale && k > sg.k0;
@@ -761,11 +761,11 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                 if (ok && __any_sync(0xffffffffu, need)) {
                     // O at rest: P.V of the block before has completed.  TMEM loads and stores are
                     // warp-wide: lanes whose row keeps its max scale by 1.
-                    ok = warp_wait(&m->p_empty[b ^ 1], ((blk - 1) >> 1) & 1, abort, wlim);
+                    if (!FP8) ok = warp_wait(&m->p_empty[b ^ 1], ((blk - 1) >> 1) & 1, abort, wlim);
                     if (ok) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                        for (int c0 = 0; c0 < VC; c0 += 32) {
                             uint32_t o[32];
                             tmem_ld32(tm_mine + c0, o);
                             tmem_wait_ld();
@@ -776,15 +776,15 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
                         tmem_wait_st();
                     }
                 }
-                lfull = fmaf(lfull, f, F16 ? (f0 + f1) / fk : f0 + f1);
-                lrun = F16 ? lfull : fmaf(lrun, f, r0 + r1);
+                lfull = fmaf(lfull, f, full.x + full.y);
+                lrun = FP8 ? lfull : fmaf(lrun, f, rounded.x + rounded.y);
                 mrun = muse;
                 if (ok) {
-                    // P row hl, chunk of this half: four 16-byte pieces of a 128-byte row (128-byte swizzle)
+                    // P row hl, chunk of this half: 16-byte pieces of a 128-byte row (128-byte swizzle)
                     uint8_t* prow = s_p + b * Cfg::P_BYTES + half * 8192 + hl * 128;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4*>(prow + (((uint32_t)(4 * part + q) ^ (uint32_t)(hl & 7)) << 4)) =
+                    for (int q = 0; q < NP / 8; ++q)
+                        *reinterpret_cast<uint4*>(prow + (((uint32_t)(NP / 8 * part + q) ^ (uint32_t)(hl & 7)) << 4)) =
                             make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                     fence_proxy_async_smem();
                     tc_fence_before();
@@ -796,13 +796,9 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             }
             // ------------------------------------------------------------ epilogue of a segment
             const bool ofull = ok && warp_wait(&m->o_full, ns & 1, abort, wlim);
-            ok = named_bar_and(1, 256, ofull);
+            ok = named_bar_and(1, SMT, ofull);
             if (!ok) break;
-            float of[4];
-            exchange(lrun, of);
-            const float ltot = (of[0] + of[1]) + (of[2] + of[3]);
-            exchange(lfull, of);
-            const float lft = (of[0] + of[1]) + (of[2] + of[3]);
+            const float ltot = row_sum(lrun), lft = FP8 ? ltot : row_sum(lfull);
             tc_fence_after();
             const bool empty = ltot == 0.0f;   // the row saw nothing here
             const int64_t row = (int64_t)sg.row0 + rr;
@@ -810,7 +806,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
             uint8_t* sl = p.part + Cfg::HEAD_BYTES +
                           ((int64_t)(2 * pair + (sg.part == 1 ? 1 : 0)) * 2 + crank) * Cfg::PART_BYTES;
 #pragma unroll 1
-            for (int c0 = 0; c0 < 128; c0 += 32) {
+            for (int c0 = 0; c0 < VC; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld32(tm_mine + c0, o);
                 tmem_wait_ld();
@@ -856,7 +852,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 1)
     if (m->abort)
         for (int i = 0; i < 100; ++i) __nanosleep(10000);
     cluster_sync();   // no remote access may target an exited CTA, and no MMA may read a freed tile
-    if (warp == Cfg::QK_WARP) {
+    if (warp == QK_WARP) {
         tc_fence_after();
         tmem_dealloc_2cta(tmem_base, Cfg::TMEM_COLS);
     }

@@ -1,0 +1,184 @@
+"""dsa_chunk_attn over an FP8 latent cache on the GPU: the shapes, masks and failures at which the
+warps that convert codes could go wrong, against dense causal attention in 64 bits over the values
+that the codes stand for (tolerances of test_chunk_gpu.reference)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import indexer_top_sparse_lightning_b200 as dsa
+from tests.paged_helpers import DV, PAGE, ROW, Paged, assert_status_ok, fp8_rows, randn
+from tests.test_chunk_gpu import SCALE, SHAPES, check, reference, run
+
+pytestmark = pytest.mark.gpu
+
+NAN = 0x7F
+
+
+def cache(pg, seed):
+    """(codes, scales, values): NaN codes, and scales NaN, infinite or huge, where nobody looks."""
+    codes, scale, val = fp8_rows(randn(seed, pg.num_blocks, PAGE, ROW))
+    used = np.zeros(pg.num_blocks * PAGE, bool)
+    for b in range(pg.B):
+        used[pg.rows(b)] = True
+    codes.view(-1, ROW)[~used] = NAN
+    other = scale.view(-1, 5)
+    other[~used] = torch.tensor([math.nan, math.inf, -math.inf, 3e38, -0.0])
+    return codes, scale, val.view(-1, ROW)
+
+
+@pytest.mark.parametrize("lens,nq,H", SHAPES)
+def test_dense_causal(lens, nq, H):
+    pg = Paged(lens, nq, seed=H + len(lens), pad=3)
+    q = randn(1 + H, pg.T, H, ROW, scale=3.0)
+    codes, scale, val = cache(pg, 2)
+    mark = torch.full((pg.T, H, DV), 5.0, dtype=torch.bfloat16, device="cuda")
+    ml = torch.full((pg.T, H), 5.0, device="cuda")
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda(), out=mark, lse=ml)
+    check(pg, out, lse, reference(pg, q, lambda b: val[pg.rows(b)], fp16=True))
+    assert (out[pg.real:] == 5).all() and (lse[pg.real:] == 5).all()      # padding rows stay
+
+
+def test_many_sequences():
+    # more sequences than threads of a block; many without new tokens
+    r = np.random.default_rng(8)
+    lens = r.integers(1, 300, size=900)
+    nq = np.minimum(lens, r.integers(0, 3, size=900))
+    pg = Paged(lens, nq, seed=1)
+    q = randn(3, pg.T, 8, ROW, scale=3.0)
+    codes, scale, val = cache(pg, 4)
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    check(pg, out, lse, reference(pg, q, lambda b: val[pg.rows(b)], fp16=True))
+
+
+def test_growing_scores():
+    # every block raises the maximum: the output so far is rescaled again and again
+    pg = Paged([1500], [40], seed=3)
+    q = randn(5, pg.T, 128, ROW).abs()
+    ramp = torch.linspace(-20, 20, 1500)[:, None]
+    x = randn(6, pg.num_blocks, PAGE, ROW)
+    x.view(-1, ROW)[pg.rows(0)] = (randn(7, 1500, ROW).float() * 0.5 + ramp * 0.1).to(torch.bfloat16)
+    codes, scale, val = fp8_rows(x)
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
+
+
+@pytest.mark.parametrize("what", ["codes", "scales"])
+@pytest.mark.parametrize("H", [16, 40, 128, 1])
+def test_later_tokens_rows_do_not_reach_earlier_ones(H, what):
+    # the last tokens' rows are not finite: every token before them is unaffected (tiles hold
+    # several tokens when H < 128), every token that sees one gets no finite result
+    n, good = 70, 50
+    pg = Paged([400], [n], seed=4)
+    q = randn(8, n, H, ROW, scale=3.0)
+    codes, scale, val = cache(pg, 9)
+    rows = pg.rows(0)
+    late = rows[400 - n + good:]
+    if what == "codes":
+        codes.view(-1, ROW)[late, 100] = NAN
+    else:
+        scale.view(-1, 5)[late, 2] = math.nan
+    clean = val.clone()
+    clean[late] = 0
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    ro, rl, bo, bl = reference(pg, q, lambda b: clean[rows], fp16=True)
+    assert ((out[:good].double() - ro[:good]).abs() <= bo[:good]).all()
+    assert ((lse[:good].double() - rl[:good]).abs() <= bl[:good]).all()
+    assert not torch.isfinite(lse[good:]).any()
+
+
+def test_bad_page_is_reported_and_not_seen():
+    pg = Paged([600, 500], [3, 20], seed=8)
+    q = randn(15, pg.T, 32, ROW, scale=3.0)
+    codes, scale, val = cache(pg, 16)
+    ref = reference(pg, q, lambda b: val[pg.rows(b)], fp16=True,
+                    hidden=lambda b: (torch.arange(int(pg.lens[b])) // PAGE == 3) if b == 1 else
+                    torch.zeros(int(pg.lens[b]), dtype=torch.bool))
+    pg.table[1, 3] = pg.num_blocks
+    ws = dsa.Workspace()
+    out, lse = dsa.dsa_chunk_attn(pg.batch(), q.cuda(), codes.cuda(), SCALE, kv_scale=scale.cuda(), workspace=ws)
+    torch.cuda.synchronize()
+    assert dsa.get_status(ws) == 6
+    check(pg, out, lse, ref)
+
+
+def test_repeats_captures_and_streams_agree():
+    # bit for bit: twice, on two streams at once, and from two graphs replayed at the same time
+    pg = Paged([5000, 900, 64, 3000], [3, 200, 1, 7], seed=9)
+    q = randn(17, pg.T, 64, ROW, scale=3.0).cuda()
+    codes, scale, _ = cache(pg, 18)
+    codes, scale = codes.cuda(), scale.cuda()
+    b = pg.batch()
+    call = lambda **kw: dsa.dsa_chunk_attn(b, q, codes, SCALE, kv_scale=scale, **kw)  # noqa: E731
+    ref, rl = call()
+    again, al = call()
+    assert torch.equal(ref, again) and torch.equal(rl, al)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [call(stream=s) for _ in range(4) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) and torch.equal(x, rl) for o, x in outs)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = call()
+        graphs.append((g, res))
+    for (g, _), s in zip(graphs, (s1, s2)):
+        with torch.cuda.stream(s):
+            g.replay()
+    assert_status_ok()
+    for _, (o, x) in graphs:
+        assert torch.equal(o, ref) and torch.equal(x, rl)
+
+
+def test_offsets_past_32_bits():
+    # the codes of the last pages lie more than 2^31 bytes into the cache
+    blocks = 2 ** 31 // (PAGE * ROW) + 40
+    pg = Paged([300], [2], seed=6)
+    q = randn(13, pg.T, 128, ROW, scale=3.0)
+    codes, scale, val = fp8_rows(randn(14, pg.num_blocks, PAGE, ROW))
+    big = torch.empty(blocks, PAGE, ROW, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(blocks, PAGE, 5, dtype=torch.float32, device="cuda")
+    big[-pg.num_blocks:], sc[-pg.num_blocks:] = codes.cuda(), scale.cuda()
+    rows = pg.rows(0)
+    pg.table[pg.table >= 0] += blocks - pg.num_blocks
+    pg.num_blocks = blocks
+    out, lse = dsa.dsa_chunk_attn(pg.batch(), q.cuda(), big, SCALE, kv_scale=sc)
+    assert_status_ok()
+    check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[rows], fp16=True))
+
+
+def test_scratch_does_not_grow_with_the_cache():
+    pg = Paged([64], [1], seed=1)
+    b = pg.batch()
+    q, codes = torch.zeros(1, 128, ROW, dtype=torch.bfloat16).cuda(), torch.zeros(pg.num_blocks, PAGE, ROW, dtype=torch.uint8).cuda()
+    sc = torch.ones(pg.num_blocks, PAGE, 5).cuda()
+    dsa.dsa_chunk_attn(b, q, codes, SCALE, kv_scale=sc)
+    table = torch.full((1, 1 << 14), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = b.block_table[0, 0]
+    long = dsa.Batch(b.seq_lens, b.cu_q, table, pg.num_blocks, 1 << 20, 1)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    dsa.dsa_chunk_attn(long, q, codes, SCALE, kv_scale=sc)
+    assert_status_ok()
+    assert torch.cuda.max_memory_allocated() - before < 64 << 20
+
+
+def test_timeout_is_reported_and_recoverable():
+    pg = Paged([3000], [4], seed=11)
+    q = randn(21, pg.T, 128, ROW).cuda()
+    codes, scale, _ = cache(pg, 22)
+    codes, scale = codes.cuda(), scale.cuda()
+    ws = dsa.Workspace()
+    call = lambda: dsa.dsa_chunk_attn(pg.batch(), q, codes, SCALE, kv_scale=scale, workspace=ws)[0]  # noqa: E731
+    clean = call()
+    assert dsa.get_status(ws) == 0
+    words = ws.buf[:16].view(torch.int32)
+    words[1], words[2] = 5000, 4
+    call()
+    assert dsa.get_status(ws) == 5                     # DSA_ERR_TIMEOUT
+    ws.reset()
+    assert torch.equal(clean, call()) and dsa.get_status(ws) == 0

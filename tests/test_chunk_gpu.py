@@ -205,6 +205,47 @@ def test_fp8_scales_of_any_size():
     check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
 
 
+@pytest.mark.parametrize("spread", [1, 6, 12])
+def test_fp8_scales_that_differ_by_tile(spread):
+    # Every tile of every position has its own power of two, 2^-spread .. 2^spread, some are zero.
+    # On top of the tolerances above: the last two tiles share an accumulator in units of u, tile
+    # 3's scale, or a 64th of the fifth's where that is more than 64 times as large.  There tile 3's
+    # codes take a factor rounded to fp16 and are rounded once more (2 * 2^-11 of them); the fifth's
+    # factor and rests are fp16 with a smallest step of 2^-24 (off by half of it, and by half of it
+    # times the code).  A value is (code f / F) F with f / F in two fp16 parts: off by 2^-25 (|code| + 1) F.
+    pg = Paged([517, 130], [3, 65], seed=13)
+    q = randn(41, pg.T, 24, ROW)
+    codes, scale, _ = fp8_rows(randn(42, pg.num_blocks, PAGE, ROW))
+    g = torch.Generator().manual_seed(spread)
+    scale *= 2.0 ** torch.randint(-spread, spread + 1, scale.shape, generator=g)
+    scale[torch.rand(scale.shape, generator=g) < 0.05] = 0.0
+    c, f = codes.view(torch.float8_e4m3fn).double().view(-1, ROW), scale.double().view(-1, 5)
+    val = c * f.repeat_interleave(128, -1)[:, :ROW]
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    ro, rl, bo, bl = reference(pg, q, lambda b: val[pg.rows(b)], fp16=True)
+    top = f[:, :4].amax(-1)
+    F = torch.where(top > 0, 2.0 ** (torch.floor(torch.log2(top.clamp_min(1e-300))) - 6), 1.0)
+    big = f[:, 4] > 64 * f[:, 3]
+    u = torch.where(big, f[:, 4] / 64, f[:, 3])
+    at = 0
+    for b in range(pg.B):
+        r, n, L = pg.rows(b), int(pg.nq[b]), int(pg.lens[b])
+        qq = q[pg.cu[b]:pg.cu[b] + n].double()
+        x = val[r]
+        dark = torch.arange(L)[None] > torch.arange(L - n, L)[:, None]
+        w = (torch.einsum("thd,sd->ths", qq, x) * SCALE).masked_fill(dark[:, None], -math.inf).softmax(-1)
+        off = torch.einsum("thd,sd->ths", qq[..., 384:512].abs(), x[:, 384:512].abs() * big[r][:, None]) * 2.0 ** -10 \
+            + torch.einsum("thd,sd->ths", qq[..., 512:].abs(), (c[r][:, 512:].abs() + 1) * u[r][:, None]) * 2.0 ** -25
+        Dx = (SCALE * off).masked_fill(dark[:, None], 0.0).amax(-1)
+        ev = 2.0 ** -25 * (c[r][:, :DV].abs() + 1) * F[r][:, None]
+        base = w @ x[:, :DV].abs()
+        more = 1.1 * torch.expm1(2 * Dx)[..., None] * (base + ro[at:at + n].abs().cpu()) + w @ ev
+        bo[at:at + n] += (more * (1 + 2.0 ** -8)).cuda()
+        bl[at:at + n] += Dx.cuda()
+        at += n
+    check(pg, out, lse, (ro, rl, bo, bl))
+
+
 def test_offsets_past_32_bits():
     # pages behind the first 4.3 GB (2^31 elements) of the cache
     pg = Paged([300, 1000], [5, 1], seed=6)
