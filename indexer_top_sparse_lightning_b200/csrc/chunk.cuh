@@ -67,7 +67,7 @@ namespace dsa {
 // brought to fp16 in shared memory: both operands of an MMA have one type, and bf16
 // would round the products of codes and scales eight times as far.  A power of two per
 // row of Q keeps it in fp16's range.  The scores are put together from four accumulators
-// here; with t_s = S_s + log2 F_s (F_s the position's power of two) the weights that multiply
+// here; with t_s = S_s + log2 F_s (F_s the page's power of two) the weights that multiply
 // the values code * f / F are P_s F_s = 2^(t_s - m), so the reference m follows t, and the
 // sums of weights are those of 2^(t_s - m) / F_s.
 template <bool FP8>
@@ -692,13 +692,9 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                         for (int i = 0; i < NP; i += 2)
                             sv[i / 2] = mul_f32x2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), make_float2(c_row, c_row));
                     } else {
-                        const float4* l4 = reinterpret_cast<const float4*>(&rec.log2f[p0]);
+                        const float2 l2 = make_float2(rec.log2f[half], rec.log2f[half]);
 #pragma unroll
-                        for (int i = 0; i < NP; i += 4) {
-                            const float4 l = l4[i / 4];
-                            sv[i / 2] = fma_f32x2(sv[i / 2], make_float2(c_row, c_row), make_float2(l.x, l.y));
-                            sv[i / 2 + 1] = fma_f32x2(sv[i / 2 + 1], make_float2(c_row, c_row), make_float2(l.z, l.w));
-                        }
+                        for (int i = 0; i < NP / 2; ++i) sv[i] = fma_f32x2(sv[i], make_float2(c_row, c_row), l2);
                     }
                     // positions of this thread that the row sees
                     const int vis = this_ok ? see - (k * Cfg::BLOCK + p0) : 0;
@@ -743,13 +739,11 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                         pk[i] = pack_bf16(e.x, e.y);
                         rounded = add_f32x2(rounded, make_float2(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
                     }
-                    if constexpr (FP8) {
-                        full = fma_f32x2(e, reinterpret_cast<const float2*>(&rec.inv[p0])[i], full);
-                    } else {
-                        full = add_f32x2(full, e);
-                    }
+                    full = add_f32x2(full, e);
                 }
+                float sum = full.x + full.y;
                 if constexpr (FP8) {
+                    sum *= rec.inv[half];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&m->rec_empty[blk % Cfg::NREC]);
                 }
@@ -776,7 +770,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                         tmem_wait_st();
                     }
                 }
-                lfull = fmaf(lfull, f, full.x + full.y);
+                lfull = fmaf(lfull, f, sum);
                 lrun = FP8 ? lfull : fmaf(lrun, f, rounded.x + rounded.y);
                 mrun = muse;
                 if (ok) {

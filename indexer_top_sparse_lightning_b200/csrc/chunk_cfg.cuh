@@ -112,11 +112,12 @@ static_assert(sizeof(ChunkMisc) <= ChunkCfg::MISC_BYTES, "misc block exceeds its
 // FP8: the factors of a block's positions (both pages), for this CTA.
 struct ChunkScales {
     float f[4][ChunkCfg::BLOCK];          // of the four score accumulators
-    float log2f[ChunkCfg::BLOCK];         // log2 F
-    float inv[ChunkCfg::BLOCK];           // 1 / F
+    float last[ChunkCfg::BLOCK];          // the fifth tile's scale
+    float log2f[2], inv[2];               // log2 F and 1 / F of the two pages
     uint32_t value[2][ChunkCfg::BLOCK];   // f_t / F of this CTA's two tiles of values, as two fp16 parts
     uint2 key[kPage];                     // g3 and g4 of this CTA's page, as two fp16 parts each
-    int ok[4];                            // the two pages' ids are good
+    int ok[2];                            // the two pages' ids are good
+    int pad[2];
 };
 // The exchange between the threads of a row lies behind the records there.
 constexpr int kChunkFp8Xm = ChunkCfg::OFF_REC + ChunkCfg::NREC * (int)sizeof(ChunkScales);

@@ -26,9 +26,10 @@
 // smaller than its neighbour).
 //
 // Values: code * f_t / F, one rounding to fp16, with F the power of two that brings
-// the largest of the position's four value scales into [64, 128), so that values end
-// below 2^16 (codes end at 448).  The weights that multiply them are P F (the softmax adds log2 F to
-// the scores and divides F out of the sums).
+// the largest value scale of the page's positions into [64, 128), so that values end
+// below 2^16 (codes end at 448); positions behind the sequence's end do not count,
+// whatever they hold.  The weights that multiply them are P F (the softmax adds log2 F to the
+// scores and divides F out of the sums).
 #pragma once
 #include <cuda_fp16.h>
 
@@ -66,6 +67,7 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
 #pragma unroll 1
         for (int k = sg.k0 - 1; k < sg.k1; ++k) {
             const int page = id;
+            float log2f = 0.0f, inv = 1.0f;
             ChunkScales& rec = ring[rr];
             if (k >= sg.k0) {
                 if (!warp_wait(&m->rec_empty[rr], ph, abort, wlim)) {
@@ -73,12 +75,24 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
                     break;
                 }
                 bad = bad || page == -2;
+                float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    const int pos = 64 * half + 32 * i + lane;
+                    const bool seen = k * Cfg::BLOCK + pos < sg.see;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) rec.f[t][64 * half + 32 * i + lane] = raw[i][t];
-                    rec.log2f[64 * half + 32 * i + lane] = raw[i][4];
+                    for (int t = 0; t < 4; ++t) {
+                        rec.f[t][pos] = raw[i][t];
+                        if (seen) top = fmaxf(top, fabsf(raw[i][t]));
+                    }
+                    rec.last[pos] = raw[i][4];
                 }
+                // magnitudes compare as integers
+                const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                int E = (int)(bits >> 23) - 127;
+                E = bits == 0 ? 6 : E < -100 ? -100 : E > 120 ? 120 : E;
+                log2f = (float)(E - 6);
+                inv = __uint_as_float((uint32_t)(6 - E + 127) << 23);
             }
             if (k + 1 < sg.k1) {
                 id = chunk_page(p, sg, table, 2 * (k + 1) + half);
@@ -95,7 +109,7 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
             if (k < sg.k0) continue;
 #pragma unroll 1
             for (int pos = 64 * half + lane; pos < 64 * half + 64; pos += 32) {
-                const float f3 = rec.f[3][pos], f4 = rec.log2f[pos];
+                const float f3 = rec.f[3][pos], f4 = rec.last[pos];
                 float u = f3, g3 = 1.0f, num = f4, den = f3;
                 const bool large = fabsf(f4) > 64.0f * fabsf(f3);
                 if (large) {
@@ -107,16 +121,14 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
                 if (large) g3 = g;
                 rec.f[3][pos] = u;
                 if (half == (int)crank) rec.key[pos & (kPage - 1)] = make_uint2(two_halves(g3), two_halves(large ? 64.0f : g));
-                const float top = fmaxf(fmaxf(fabsf(rec.f[0][pos]), fabsf(rec.f[1][pos])), fmaxf(fabsf(rec.f[2][pos]), fabsf(f3)));
-                int E = (int)(__float_as_uint(top) >> 23) - 127;
-                E = top == 0.0f ? 6 : E < -100 ? -100 : E > 120 ? 120 : E;
-                const float inv = __uint_as_float((uint32_t)(6 - E + 127) << 23);
-                rec.log2f[pos] = (float)(E - 6);
-                rec.inv[pos] = inv;
                 rec.value[0][pos] = two_halves(rec.f[2 * crank][pos] * inv);
                 rec.value[1][pos] = two_halves((crank == 0 ? rec.f[1][pos] : f3) * inv);
             }
-            if (lane == 0) rec.ok[half] = page != -2;
+            if (lane == 0) {
+                rec.log2f[half] = log2f;
+                rec.inv[half] = inv;
+                rec.ok[half] = page != -2;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->rec_full[rr]);
             if (++rr == Cfg::NREC) {

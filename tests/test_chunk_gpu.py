@@ -212,7 +212,8 @@ def test_fp8_scales_that_differ_by_tile(spread):
     # 3's scale, or a 64th of the fifth's where that is more than 64 times as large.  There tile 3's
     # codes take a factor rounded to fp16 and are rounded once more (2 * 2^-11 of them); the fifth's
     # factor and rests are fp16 with a smallest step of 2^-24 (off by half of it, and by half of it
-    # times the code).  A value is (code f / F) F with f / F in two fp16 parts: off by 2^-25 (|code| + 1) F.
+    # times the code).  A value is (code f / F) F, F the page's power of two, with f / F in two fp16 parts:
+    # off by 2^-25 (|code| + 1) F.
     pg = Paged([517, 130], [3, 65], seed=13)
     q = randn(41, pg.T, 24, ROW)
     codes, scale, _ = fp8_rows(randn(42, pg.num_blocks, PAGE, ROW))
@@ -223,7 +224,9 @@ def test_fp8_scales_that_differ_by_tile(spread):
     val = c * f.repeat_interleave(128, -1)[:, :ROW]
     out, lse = run(pg, q, codes, kv_scale=scale.cuda())
     ro, rl, bo, bl = reference(pg, q, lambda b: val[pg.rows(b)], fp16=True)
-    top = f[:, :4].amax(-1)
+    used = torch.zeros(len(f), dtype=torch.bool)
+    used[np.concatenate([pg.rows(b) for b in range(pg.B)])] = True
+    top = (f[:, :4].amax(-1) * used).view(-1, PAGE).amax(-1).repeat_interleave(PAGE)
     F = torch.where(top > 0, 2.0 ** (torch.floor(torch.log2(top.clamp_min(1e-300))) - 6), 1.0)
     big = f[:, 4] > 64 * f[:, 3]
     u = torch.where(big, f[:, 4] / 64, f[:, 3])
