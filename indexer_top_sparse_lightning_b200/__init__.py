@@ -538,7 +538,7 @@ def status_workspace(device=None) -> Workspace:
 def _status(ws: Optional[Workspace], dev: int) -> int:
     """Pointer of a call's status area, on the device that is current."""
     if ws is None:
-        return status_workspace(dev).get(256).data_ptr()
+        ws = _status_ws.get(dev) or status_workspace(dev)
     t = ws.get(256)
     if t.get_device() != dev:
         raise ValueError(f"the workspace is on {t.device}, the tensors on cuda:{dev}")
@@ -580,46 +580,47 @@ def _dense(t, name, dtype, shape, dev: int) -> int:
 
 
 def _vector(t, name, dtype, dev: int):
-    """(pointer, length) of a dense vector, (None, 0) for None."""
-    if t is None:
-        return None, 0
-    n = t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 1 else None
-    return _dense(t, name, dtype, (n,), dev), n
+    """(pointer, length) of a dense vector."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.get_device() == dev >= 0 \
+            and t.is_contiguous():
+        return t.data_ptr(), t.numel()
+    _check(t, name, dtype, 1)
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
 
 
 def _batch_struct(batch: Batch, T: int, dev: int) -> _Batch:
     """The batch's argument block, its tensors checked."""
-    t = batch.seq_lens
-    B = t.shape[0] if t.dim() == 1 else None
-    table = batch.block_table
-    W = table.shape[1] if table.dim() == 2 else None
-    i32 = torch.int32
-    return _Batch(B, T, _dense(t, "seq_lens", i32, (B,), dev), _dense(batch.cu_q, "cu_q", i32, (B + 1,), dev),
-                  _dense(table, "block_table", i32, (B, W), dev), W, batch.num_blocks, batch.max_seq_len,
-                  batch.max_q_per_seq)
+    i32, table = torch.int32, batch.block_table
+    lens, B = _vector(batch.seq_lens, "seq_lens", i32, dev)
+    cu, n = _vector(batch.cu_q, "cu_q", i32, dev)
+    if n != B + 1:
+        raise ValueError(f"cu_q dim 0 must be {B + 1}, got {n}")
+    W = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else None
+    return _Batch(B, T, lens, cu, _dense(table, "block_table", i32, (B, W), dev), W, batch.num_blocks,
+                  batch.max_seq_len, batch.max_q_per_seq)
 
 
 def _rows(t, name, ndim: int, dev: int):
-    """Shape and strides of a bf16 CUDA tensor of dense, 16-byte aligned rows (other strides may be any)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
+    """Pointer, shape and strides of a bf16 CUDA tensor of dense, 16-byte aligned rows (other strides may be any)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == ndim and t.get_device() == dev >= 0):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
         raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
-    shape, strides = t.shape, t.stride()
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(shape)}")
+    shape, strides, p = t.shape, t.stride(), t.data_ptr()
     if not t.is_contiguous():
         # the stride of a dimension of one element is never used
         strides = [s if n > 1 else 0 for n, s in zip(shape, strides)]
         if (shape[-1] > 1 and strides[-1] != 1) or any(s % 8 for s in strides[:-1]):
             raise ValueError(f"{name} needs dense rows 16 bytes apart, got strides {t.stride()}")
-    if t.data_ptr() % 16:
+    if p % 16:
         raise ValueError(f"{name} must be 16-byte aligned")
-    return shape, strides
+    return p, shape, strides
 
 
 def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_gamma=None, eps: float = 1e-6,
@@ -638,28 +639,31 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
         raise ValueError("q or k is needed")
     dev = main.get_device() if isinstance(main, torch.Tensor) else -1
     f32 = torch.float32
-    H = qp = kp = cp = sp = 0
+    H = qp = kp = cp = sp = qn = kn = R = 0
     qs, ks, kt = (0, 0), (0,), KV_BF16
+    qg = kg = fp = pp = None
     if q is not None:
-        (T, H, D), qs = _rows(q, "q", 3, dev)
-        qp = q.data_ptr()
+        qp, (T, H, D), qs = _rows(q, "q", 3, dev)
     if k is not None:
-        shape, ks = _rows(k, "k", 2, dev)
+        kp, shape, ks = _rows(k, "k", 2, dev)
         if q is not None and shape != (T, D):
             raise ValueError(f"k {tuple(shape)} does not match q {tuple(q.shape)}")
         T, D = shape
-        kp = k.data_ptr()
         if k_scale is None:
             cp = _dense(k_cache, "k_cache", torch.bfloat16, (batch.num_blocks, 64, D), dev)
         else:
             kt = KV_FP8
             cp = _dense(k_cache, "k_cache", torch.uint8, (batch.num_blocks, 64, D), dev)
             sp = _dense(k_scale, "k_scale", f32, (batch.num_blocks, 64, 5), dev)
-    qg, qn = _vector(q_gamma, "q_gamma", f32, dev)
-    kg, kn = _vector(k_gamma, "k_gamma", f32, dev)
-    fp, R = _vector(inv_freq, "inv_freq", f32, dev)
-    R *= 2
-    pp = None if positions is None else _dense(positions, "positions", torch.int32, (T,), dev)
+    if q_gamma is not None:
+        qg, qn = _vector(q_gamma, "q_gamma", f32, dev)
+    if k_gamma is not None:
+        kg, kn = _vector(k_gamma, "k_gamma", f32, dev)
+    if inv_freq is not None:
+        fp, R = _vector(inv_freq, "inv_freq", f32, dev)
+        R *= 2
+    if positions is not None:
+        pp = _dense(positions, "positions", torch.int32, (T,), dev)
     cb = _batch_struct(batch, T, dev)
     s = _Rope(qp, qs[0], qs[1], kp, ks[0], H, D, qg, kg, qn, kn, eps, fp, R,
               D - R if rope_off is None else rope_off, bool(interleaved), pp, kt)
@@ -668,10 +672,12 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
         op = 0
         if q is not None:
             if q_out is None:
-                q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=main.device)
-            op = _dense(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
-            if op == qp and not q.is_contiguous():
-                raise ValueError("q_out may be q only when q is contiguous")
+                q_out = torch.empty_like(q) if q.is_contiguous() else torch.empty(T, H, D, dtype=q.dtype, device=q.device)
+                op = q_out.data_ptr()
+            else:
+                op = _dense(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
+                if op == qp and not q.is_contiguous():
+                    raise ValueError("q_out may be q only when q is contiguous")
         rc = lib.dsa_qk_norm_rope(ctypes.byref(cb), ctypes.byref(s), op, cp, sp, status, on)
     if rc != 0:
         raise DsaError(rc, "dsa_qk_norm_rope")
@@ -709,11 +715,15 @@ def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None,
         if need == 0:
             raise DsaError(2, "dsa_chunk_scratch_size")
         if out is None:
-            out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=q.device)
+            op = out.data_ptr()
+        else:
+            op = _dense(out, "out", torch.bfloat16, (T, H, 512), dev)
         if lse is None and want_lse:
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-        op = _dense(out, "out", torch.bfloat16, (T, H, 512), dev)
-        lp = None if lse is None else _dense(lse, "lse", torch.float32, (T, H), dev)
+            lse = torch.empty(T, H, dtype=torch.float32, device=q.device)
+            lp = lse.data_ptr()
+        else:
+            lp = None if lse is None else _dense(lse, "lse", torch.float32, (T, H), dev)
         scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
         rc = lib.dsa_chunk_attn(ctypes.byref(cb), ctypes.byref(at), op, lp, status, scratch.data_ptr(), need, on)
     if rc != 0:
