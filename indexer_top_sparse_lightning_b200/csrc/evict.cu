@@ -53,11 +53,12 @@ dsa_status check_evict(const dsa_batch* bt, const dsa_evict_inputs* in, const in
 
 namespace {
 
-// CTAs per sequence of the wide kernels (0: the cluster kernel serves), and their scratch.
+// CTAs per sequence of the wide kernel (0: the cluster kernel serves): at least kEvictWideRange
+// positions each, and all sequences at once where there are enough SMs.
 int wide_ctas(const dsa_batch* bt, const DevInfo& di) {
     if (bt->max_seq_len < kEvictWide) return 0;
     const int by_len = (int)(((int64_t)bt->max_seq_len + kEvictWideRange - 1) / kEvictWideRange);
-    const int by_sms = di.sms / bt->batch > 8 ? di.sms / bt->batch : 8;
+    const int by_sms = di.sms / bt->batch > 8 ? di.sms / bt->batch : di.sms < 8 ? di.sms : 8;
     return by_len < by_sms ? by_len : by_sms;
 }
 
@@ -69,7 +70,7 @@ size_t dsa_evict_scratch_size(const dsa_batch* batch) {
     if (check_batch(batch) != DSA_OK) return 0;
     const DevInfo di = dev_info();
     if (di.sms <= 0) return 0;
-    return 256 + align256((size_t)batch->batch * (3 * kEvictBins + 2 * (size_t)wide_ctas(batch, di)) * 4);
+    return 256 + align256(((size_t)di.sms + (size_t)batch->batch * (3 * kEvictBins + 2 * (size_t)wide_ctas(batch, di))) * 4);
 }
 
 dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, int32_t* out_idx, int32_t* out_len, void* status,
@@ -122,17 +123,20 @@ dsa_status dsa_cache_evict(const dsa_batch* batch, const dsa_evict_inputs* in, i
     cfg.attrs = attr;
     p.ctas = wide_ctas(batch, di);
     if (p.ctas) {
-        p.hist = static_cast<uint32_t*>(scratch);
+        const int groups = di.sms / p.ctas < p.B ? di.sms / p.ctas : p.B;
+        p.barriers = static_cast<uint32_t*>(scratch);
+        p.hist = p.barriers + di.sms;
         p.counts = p.hist + (size_t)p.B * 3 * kEvictBins;
-        if (cudaError_t e = cudaMemsetAsync(p.hist, 0, (size_t)p.B * 3 * kEvictBins * 4, s))
+        if (cudaError_t e = cudaMemsetAsync(scratch, 0, ((size_t)di.sms + (size_t)p.B * 3 * kEvictBins) * 4, s))
             return fail(DSA_ERR_CUDA, "eviction histogram clear", e);
-        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)p.B, 1);
-        void (*const steps[5])(EvictParams) = {&evict_wide_kernel<0>, &evict_wide_kernel<1>, &evict_wide_kernel<2>,
-                                               &evict_wide_kernel<3>, &evict_wide_kernel<4>};
-        for (int i = 0; i < 5; ++i) {
-            cfg.numAttrs = i == 0 ? 0 : 1;      // (the first follows the clear in stream order)
-            if (cudaError_t e = cudaLaunchKernelEx(&cfg, steps[i], p)) return fail(DSA_ERR_CUDA, "eviction choice launch", e);
-        }
+        cudaLaunchAttribute together;                    // the CTAs of a group wait for one another
+        together.id = cudaLaunchAttributeCooperative;
+        together.val.cooperative = 1;
+        cfg.gridDim = dim3((unsigned)(groups * p.ctas), 1, 1);
+        cfg.attrs = &together;
+        cfg.numAttrs = 1;
+        if (cudaError_t e = cudaLaunchKernelEx(&cfg, &evict_wide_kernel, p)) return fail(DSA_ERR_CUDA, "eviction choice launch", e);
+        cfg.attrs = attr;
     } else {
         p.cluster = 1;
         while (p.cluster < 8 && (int64_t)p.cluster * 8192 < batch->max_seq_len) p.cluster *= 2;

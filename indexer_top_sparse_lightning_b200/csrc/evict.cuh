@@ -15,10 +15,10 @@
 // common: they are counted with ballots, since a histogram bin that a whole warp
 // adds to takes its lanes one by one.
 //
-// Longer sequences (kEvictWide positions and more) take the same steps as launches of
-// their own over many CTAs (evict_wide_kernel: three digits, counts, lists), joined
-// through histograms in scratch: eight CTAs would need 270 us for a million
-// positions, most of it histogram adds, which a CTA takes one by one.
+// Longer sequences (kEvictWide positions and more) take the same steps with a group of up to
+// all SMs' CTAs each (evict_wide_kernel), joined through histograms and counts in
+// scratch: eight CTAs would need 270 us for a million positions, most of it histogram
+// adds, which a CTA takes one by one.
 //
 // evict_copy_kernel: memory-bound, every kept row read and written once.  A block
 // takes 32 rows: their places are resolved once, then each array's rows are copied
@@ -65,9 +65,10 @@ struct EvictParams {
     int32_t cluster;          // CTAs per sequence
     int32_t cache;            // keys of a CTA's range at most (in shared memory)
     int32_t n_arrays;
-    // the wide kernels: CTAs per sequence, and [B][3][2048] digit counts (zero at first), then
-    // [B][ctas][2] counts of keys above and equal
+    // the wide kernel: CTAs per group; a barrier count per group and [B][3][2048] digit counts
+    // (zero at first), then [B][ctas][2] counts of keys above and equal
     int32_t ctas;
+    uint32_t* barriers;
     uint32_t* hist;
     uint32_t* counts;
     EvictArray arrays[kEvictMaxArrays];
@@ -80,6 +81,7 @@ struct EvictShared {
     uint32_t cta_gt, cta_eq;  // of this CTA's range
     uint32_t digit, above;    // result of a digit's search
     uint32_t gt_before, eq_before;
+    int arrived;              // the group's barrier was passed
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32_t rank) {
@@ -277,94 +279,116 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(const __
     evict_emit(s, out, lo, w0, w1, prefix, need, key_at);
 }
 
-// The wide kernels.  STEP 0..2: the histogram of a digit among the keys that share
-// the digits before; 3: the keys above and equal to the threshold in this CTA's
-// range; 4: the list.  Every step finds the digits again from the histograms.
-template <int STEP>
+// Waits until all CTAs of the group have arrived `target` times in all.  False (and reported)
+// after the wait limit.
+__device__ __forceinline__ bool evict_group_barrier(const EvictParams& p, EvictShared* s, uint32_t* count, uint32_t target) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atom_add_acq_rel_gpu(count, 1u);
+        const uint32_t us = __ldcg(p.status + 1);        // test hook: wait limit in microseconds
+        const uint64_t limit = us ? (uint64_t)us * 1000u : kWaitTimeoutNs, t0 = globaltimer();
+        s->arrived = 1;
+        while (ld_acquire_gpu(count) < target)
+            if (globaltimer() - t0 > limit) {
+                s->arrived = 0;
+                atomicCAS(p.status, 0u, (uint32_t)kStTimeout);
+                break;
+            }
+    }
+    __syncthreads();
+    return s->arrived != 0;
+}
+
+// Long sequences: a group of CTAs each, all groups at once (a cooperative launch), a group's
+// sequences one after another.  The steps are those of the cluster kernel, joined through
+// histograms and counts in scratch and a barrier of the group; a CTA's keys are read
+// again in every step (they stay in L2).
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __grid_constant__ EvictParams p) {
     __shared__ EvictShared s_all;
     EvictShared* s = &s_all;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = (int)blockIdx.y, cta = (int)blockIdx.x;
-    griddep_launch_dependents();
-    griddep_wait();
-    const int L = evict_len(p, b), keep = p.keep;
-    int32_t* out = p.idx + (int64_t)b * keep;
-    if (STEP == 4 && cta == 0 && threadIdx.x == 0) p.len[b] = L < keep ? L : keep;
-    if (L <= keep) {
-        if (STEP == 4)
-            for (int64_t i = (int64_t)cta * kEvictThreads + threadIdx.x; i < keep; i += (int64_t)p.ctas * kEvictThreads)
-                out[i] = i < L ? (int32_t)i : -1;
-        return;
-    }
-    const int per = (L + p.ctas - 1) / p.ctas;
-    const int64_t lo64 = (int64_t)per * cta;
-    const int lo = lo64 < L ? (int)lo64 : L;
-    const int n = L - lo < per ? L - lo : per;
-    const float* w = p.weight + (int64_t)b * p.stride + lo;
-    auto key_at = [&](int i) -> uint32_t {
-        const float x = __ldg(w + i);
-        const int pos = lo + i;
-        if (pos < p.sink || pos >= L - p.recent) return 0xFFFFFFFFu;
-        return x != x ? 0u : order_key(x);
-    };
+    const int group = (int)blockIdx.x / p.ctas, cta = (int)blockIdx.x % p.ctas;
+    const int groups = (int)gridDim.x / p.ctas, keep = p.keep;
     constexpr uint32_t ZERO = 0x80000000u;               // order_key(0)
     constexpr int BATCH = 4;
-    constexpr int SHIFT[3] = {21, 10, 0};
-    uint32_t* hist = p.hist + (int64_t)b * 3 * kEvictBins;
-
-    uint32_t prefix = 0, need = (uint32_t)keep;
-#pragma unroll
-    for (int d = 0; d < (STEP < 3 ? STEP : 3); ++d) {
-        const int bin1 = kEvictBins - 1 - 2 * (int)threadIdx.x, bin0 = bin1 - 1;
-        const uint32_t c1 = __ldcg(hist + d * kEvictBins + bin1), c0 = __ldcg(hist + d * kEvictBins + bin0);
-        uint32_t x = c1 + c0;
-#pragma unroll
-        for (int e = 1; e < 32; e <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, e);
-            if (lane >= e) x += y;
+    uint32_t* barrier = p.barriers + group;
+    uint32_t arrivals = 0;
+    for (int b = group; b < p.B; b += groups) {
+        const int L = evict_len(p, b);
+        int32_t* out = p.idx + (int64_t)b * keep;
+        if (cta == 0 && threadIdx.x == 0) p.len[b] = L < keep ? L : keep;
+        if (L <= keep) {
+            for (int64_t i = (int64_t)cta * kEvictThreads + threadIdx.x; i < keep; i += (int64_t)p.ctas * kEvictThreads)
+                out[i] = i < L ? (int32_t)i : -1;
+            continue;
         }
-        if (lane == 31) s->warp_sum[warp] = x;
-        __syncthreads();
-        uint32_t before = x - (c1 + c0);
-        before += sum_before(s->warp_sum);
-        if (before < need && need <= before + c1) {
-            s->digit = (uint32_t)bin1;
-            s->above = before;
-        } else if (before + c1 < need && need <= before + c1 + c0) {
-            s->digit = (uint32_t)bin0;
-            s->above = before + c1;
-        }
-        __syncthreads();
-        prefix |= s->digit << SHIFT[d];
-        need -= s->above;
-        __syncthreads();
-    }
-    if constexpr (STEP < 3) {
-        constexpr uint32_t above_mask = STEP == 0 ? 0u : STEP == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-        constexpr uint32_t mask = STEP == 2 ? 1023u : 2047u;
-        for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads) s->hist[i] = 0;
-        __syncthreads();
-        uint32_t zeros = 0;
-        for (int i0 = 0; i0 < n; i0 += kEvictThreads * BATCH) {
-            uint32_t k[BATCH];
+        const int per = (L + p.ctas - 1) / p.ctas;
+        const int64_t lo64 = (int64_t)per * cta;
+        const int lo = lo64 < L ? (int)lo64 : L;
+        const int n = L - lo < per ? L - lo : per;
+        const float* w = p.weight + (int64_t)b * p.stride + lo;
+        auto key_at = [&](int i) -> uint32_t {
+            const float x = __ldg(w + i);
+            const int pos = lo + i;
+            if (pos < p.sink || pos >= L - p.recent) return 0xFFFFFFFFu;
+            return x != x ? 0u : order_key(x);
+        };
+        uint32_t prefix = 0, need = (uint32_t)keep;
+#pragma unroll 1
+        for (int d = 0; d < 3; ++d) {
+            const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+            const uint32_t mask = d == 2 ? 1023u : 2047u;
+            const uint32_t above_mask = d == 0 ? 0u : d == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+            uint32_t* hist = p.hist + ((int64_t)b * 3 + d) * kEvictBins;
+            for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads) s->hist[i] = 0;
+            __syncthreads();
+            uint32_t zeros = 0;
+            for (int i0 = 0; i0 < n; i0 += kEvictThreads * BATCH) {
+                uint32_t k[BATCH];
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-                const int i = i0 + u * kEvictThreads + (int)threadIdx.x;
-                k[u] = i < n ? key_at(i) : 0u;
+                for (int u = 0; u < BATCH; ++u) {
+                    const int i = i0 + u * kEvictThreads + (int)threadIdx.x;
+                    k[u] = i < n ? key_at(i) : 0u;
+                }
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                    const bool here = i0 + u * kEvictThreads + (int)threadIdx.x < n && (k[u] & above_mask) == prefix;
+                    zeros += __popc(__ballot_sync(0xffffffffu, here && k[u] == ZERO));
+                    if (here && k[u] != ZERO) atomicAdd(&s->hist[(k[u] >> shift) & mask], 1u);
+                }
             }
+            if (lane == 0 && zeros) atomicAdd(&s->hist[(ZERO >> shift) & mask], zeros);
+            __syncthreads();
+            for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads)
+                if (s->hist[i]) atomicAdd(hist + i, s->hist[i]);
+            if (!evict_group_barrier(p, s, barrier, arrivals += p.ctas)) return;
+            // the bin that holds the need-th key, highest bins first, two a thread
+            const int bin1 = kEvictBins - 1 - 2 * (int)threadIdx.x, bin0 = bin1 - 1;
+            const uint32_t c1 = __ldcg(hist + bin1), c0 = __ldcg(hist + bin0);
+            uint32_t x = c1 + c0;
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-                const bool here = i0 + u * kEvictThreads + (int)threadIdx.x < n && (k[u] & above_mask) == prefix;
-                zeros += __popc(__ballot_sync(0xffffffffu, here && k[u] == ZERO));
-                if (here && k[u] != ZERO) atomicAdd(&s->hist[(k[u] >> SHIFT[STEP]) & mask], 1u);
+            for (int e = 1; e < 32; e <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, e);
+                if (lane >= e) x += y;
             }
+            if (lane == 31) s->warp_sum[warp] = x;
+            __syncthreads();
+            uint32_t before = x - (c1 + c0);
+            before += sum_before(s->warp_sum);
+            if (before < need && need <= before + c1) {
+                s->digit = (uint32_t)bin1;
+                s->above = before;
+            } else if (before + c1 < need && need <= before + c1 + c0) {
+                s->digit = (uint32_t)bin0;
+                s->above = before + c1;
+            }
+            __syncthreads();
+            prefix |= s->digit << shift;
+            need -= s->above;
+            __syncthreads();
         }
-        if (lane == 0 && zeros) atomicAdd(&s->hist[(ZERO >> SHIFT[STEP]) & mask], zeros);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads)
-            if (s->hist[i]) atomicAdd(hist + STEP * kEvictBins + i, s->hist[i]);
-    } else {
+        // keys above `prefix` stay, and `need` of those equal to it, lowest positions first
         const int span = (n + kEvictWarps - 1) / kEvictWarps;
         const int w0 = warp * span < n ? warp * span : n, w1 = w0 + span < n ? w0 + span : n;
         uint32_t gt = 0, eq = 0;
@@ -387,33 +411,30 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __gr
             s->warp_eq[warp] = eq;
         }
         __syncthreads();
-        if constexpr (STEP == 3) {
-            const uint32_t g = sum_all(s->warp_gt), e = sum_all(s->warp_eq);
-            if (threadIdx.x == 0) {
-                p.counts[2 * ((int64_t)b * p.ctas + cta)] = g;
-                p.counts[2 * ((int64_t)b * p.ctas + cta) + 1] = e;
-            }
-        } else {
-            // counts of the CTAs before, then of the warps before
-            if (warp == 0) {
-                uint32_t g = 0, e = 0;
-                for (int q = lane; q < cta; q += 32) {
-                    g += __ldcg(p.counts + 2 * ((int64_t)b * p.ctas + q));
-                    e += __ldcg(p.counts + 2 * ((int64_t)b * p.ctas + q) + 1);
-                }
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) {
-                    g += __shfl_xor_sync(0xffffffffu, g, d);
-                    e += __shfl_xor_sync(0xffffffffu, e, d);
-                }
-                if (lane == 0) {
-                    s->gt_before = g;
-                    s->eq_before = e;
-                }
-            }
-            __syncthreads();
-            evict_emit(s, out, lo, w0, w1, prefix, need, key_at);
+        uint32_t* counts = p.counts + 2 * (int64_t)b * p.ctas;
+        const uint32_t g_all = sum_all(s->warp_gt), e_all = sum_all(s->warp_eq);
+        if (threadIdx.x == 0) {
+            counts[2 * cta] = g_all;
+            counts[2 * cta + 1] = e_all;
         }
+        if (!evict_group_barrier(p, s, barrier, arrivals += p.ctas)) return;
+        // counts of the CTAs before
+        if (warp == 0) {
+            uint32_t g = 0, e = 0;
+            for (int q = lane; q < cta; q += 32) {
+                g += __ldcg(counts + 2 * q);
+                e += __ldcg(counts + 2 * q + 1);
+            }
+            g = __reduce_add_sync(0xffffffffu, g);
+            e = __reduce_add_sync(0xffffffffu, e);
+            if (lane == 0) {
+                s->gt_before = g;
+                s->eq_before = e;
+            }
+        }
+        __syncthreads();
+        evict_emit(s, out, lo, w0, w1, prefix, need, key_at);
+        __syncthreads();             // the sums are free for the next sequence
     }
 }
 

@@ -191,3 +191,36 @@ def test_refusals():
         dsa.dsa_cache_evict(b, w[:, :200].contiguous(), 100, t, [], [])
     with pytest.raises(ValueError):
         dsa.dsa_cache_evict(b, w, 100, t, [torch.zeros(1, 64, 4, device="cuda")], [torch.zeros(2, 64, 4, device="cuda")])
+
+
+def test_long_sequences_in_turns():
+    # more long sequences than groups of CTAs, some short ones among them
+    r = np.random.default_rng(21)
+    lens = [70000 if i % 3 else 900 for i in range(40)]
+    lens[5] = 69999
+    check(lens, 2000, 4, 64, "ties", seed=22, arrays=ARRAYS[4:5])
+
+
+def test_long_sequences_captured_and_on_two_streams():
+    pg = Paged([300000, 200], [1, 1], seed=23)
+    w = torch.from_numpy(weights(2, 300000, 24)).cuda()
+    b = pg.batch()
+    table = torch.zeros(2, 160, dtype=torch.int32, device="cuda")
+    call = lambda **kw: dsa.dsa_cache_evict(b, w, 10000, table, [], [], sink=3, **kw)[0]  # noqa: E731
+    idx = call()
+    np.testing.assert_array_equal(idx[0].cpu().numpy(), choose(w[0].cpu().numpy(), 300000, 10000, 3, 0))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    many = [call(stream=s) for _ in range(10) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, call()))
+    for (g, _), s in zip(graphs, (s1, s2)):
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                g.replay()
+    assert_status_ok()
+    assert all(torch.equal(idx, x) for x in many + [x for _, x in graphs])
