@@ -774,14 +774,15 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
         raise ValueError(f"keep {keep} has no room for sink {sink} and recent {recent}")
     if len(arrays) != len(new_arrays):
         raise ValueError(f"{len(arrays)} arrays, {len(new_arrays)} new ones")
-    new_blocks = int(new_arrays[0].shape[0]) if len(new_arrays) else max(1, B * W)
+    old_blocks, new_blocks = batch.num_blocks, new_arrays[0].shape[0] if len(new_arrays) else max(1, B * W)
     copies = (_CacheArray * max(1, len(arrays)))()
     for i, (a, c) in enumerate(zip(arrays, new_arrays)):
         if not isinstance(a, torch.Tensor) or a.dim() < 2:
             raise ValueError(f"arrays[{i}] must be a tensor [num_blocks, 64, ...]")
-        ap = _dense(a, f"arrays[{i}]", a.dtype, (batch.num_blocks, 64) + tuple(a.shape[2:]), dev)
-        cp = _dense(c, f"new_arrays[{i}]", a.dtype, (new_blocks, 64) + tuple(a.shape[2:]), dev)
-        copies[i] = _CacheArray(ap, cp, a[0, 0].numel() * a.element_size())
+        row, e = a.shape[2:], copies[i]
+        e.src = _dense(a, f"arrays[{i}]", a.dtype, (old_blocks, 64) + row, dev)
+        e.dst = _dense(c, f"new_arrays[{i}]", a.dtype, (new_blocks, 64) + row, dev)
+        e.row_bytes = a.nbytes // (64 * old_blocks) if old_blocks else 0
     np_, nn = None, 0
     if new_weight is not None:
         nn = new_weight.shape[1] if isinstance(new_weight, torch.Tensor) and new_weight.dim() == 2 else None
@@ -790,11 +791,15 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
     with _On(dev, stream) as on:
         status = _status(workspace, dev)
         if out_idx is None:
-            out_idx = torch.empty((B, keep), dtype=torch.int32, device=weight.device)
+            out_idx = torch.empty(B, keep, dtype=torch.int32, device=weight.device)
+            ip = out_idx.data_ptr()
+        else:
+            ip = _dense(out_idx, "out_idx", torch.int32, (B, keep), dev)
         if out_len is None:
             out_len = torch.empty(B, dtype=torch.int32, device=weight.device)
-        ip = _dense(out_idx, "out_idx", torch.int32, (B, keep), dev)
-        lp = _dense(out_len, "out_len", torch.int32, (B,), dev)
+            lp = out_len.data_ptr()
+        else:
+            lp = _dense(out_len, "out_len", torch.int32, (B,), dev)
         need = lib.dsa_evict_scratch_size(ctypes.byref(cb))
         scratch = torch.empty(max(need, 256), dtype=torch.uint8, device=weight.device)
         rc = lib.dsa_cache_evict(ctypes.byref(cb), ctypes.byref(s), ip, lp, status, scratch.data_ptr(), need, on)

@@ -4,9 +4,11 @@
 // What bounds it: instructions and shared memory.  A block's 70 KB of codes per CTA become 144
 // KB of operands; the converting and softmax warps issue in 61 % of the cycles and the
 // shared-memory pipe is half busy with them, beside the MMAs' own reads (tensor pipes 24 %).
-// Two tokens of 8 sequences of 16K to 128K positions take 547 us, two tiles of 128 rows
-// over 530K positions; one pass over an fp16 copy of the cache in global memory, which wrote and
-// read 2304 bytes a position, took 930 with the copy.
+// Two tokens of 8 sequences of 16K to 128K positions take 545 us, two tiles of 128 rows
+// over 530K positions; over an fp16 copy of the cache in global memory, which wrote and
+// read 2304 bytes a position, they took 900 with the copy.  Many tiles over one short
+// sequence favoured the copy, which then stayed in L2 (2048 tokens at 16K: 10.9 ms, here
+// 15.6); it was given up for its scratch, 2304 bytes for every position of the batch.
 //
 // Two teams of CONV_WARPS warps convert, one the keys and one the values, a ring group
 // (16 KB of fp16, 8 KB of codes) at a time; the codes of the groups behind are on their way to
@@ -224,10 +226,10 @@ __device__ __forceinline__ bool fp8_codes(const ChunkParams& p, ChunkMisc* m, ui
 
 // Keys of this CTA's page of every block: groups in the order fifth tile (rests, then
 // values: the small ones first), tile 3, tiles 0 to 2; each two chunks of [64 rows x 64].
-// A thread takes 16 codes at a time; eight
-// neighbouring lanes take four pieces of two rows, of different halves of the 128, which keeps
-// both their reads and their writes on different banks.  Loops are rolled: unrolled code of
-// this many roles does not fit the instruction cache, and ran at a third of this speed.
+// A thread takes 16 codes at a time; eight neighbouring lanes take four pieces of two rows,
+// of different halves of the 128, which keeps both their reads and their writes on
+// different banks.  The loops over groups are rolled: unrolled code of this many roles does not
+// fit the instruction cache, and ran at half of this speed.
 __device__ __forceinline__ bool fp8_keys(const ChunkParams& p, ChunkMisc* m, uint8_t* smem, int ti, uint32_t crank,
                                          volatile int* abort, uint64_t wlim) {
     using Cfg = ChunkCfg;

@@ -23,6 +23,12 @@
 // evict_copy_kernel: memory-bound, every kept row read and written once.  A block
 // takes 32 rows: their places are resolved once, then each array's rows are copied
 // in 16-byte pieces (or what their width allows), four loads in flight per thread.
+// (Blocks that stay and resolve the next rows' places while they copy were slower, 185 for
+// 147 us below.)
+//
+// Measured: 32 sequences of 28K to 32K cut to 8192 positions, latent rows and index keys,
+// 147 us: 24 to choose, 122 to copy 740 MB (6.07 TB/s).  A million positions cut to 65536, FP8 rows:
+// 61 us, about half each for the choice and the copy.
 #pragma once
 #include "common.h"
 #include "paging.cuh"

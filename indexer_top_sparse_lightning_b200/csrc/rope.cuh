@@ -8,7 +8,9 @@
 // with pairs (i, i + R/2) ("halves") or (2i, 2i + 1) ("interleaved").
 //
 // What bounds it: memory.  Each row is read once and written once (D * 2 bytes
-// each way); the arithmetic is a few operations per element.
+// each way); the arithmetic is a few operations per element.  8192 tokens of 128 heads of
+// 576 with their keys take 462 us, 5.27 TB/s of the 6.56 of a plain copy.  A decode step
+// is bound by the call: 32 tokens take 7 us on the device, 14 with the host's work.
 //
 // Layout.  Eight lanes share a row, 16 bytes (8 elements) per lane and round,
 // so a round of the eight lanes is one 128-byte line and a row of D elements
@@ -154,7 +156,8 @@ __device__ __forceinline__ void turned8(const uint16_t* x, uint4 v, int e, const
 // row, kRopeGroups rows at a time); the blocks behind them: the key rows of
 // ktpc tokens each.  Query blocks of one token's heads share its angle table.
 template <int NV>
-__global__ void __launch_bounds__(kRopeThreads, NV <= 2 ? 6 : NV <= 4 ? 4 : NV <= 9 ? 3 : 2) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, NV <= 2 ? 6 : NV <= 4 ? 4 : NV <= 9 ? 3 : 2)
+    qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 s_cs[kRopeTable];
     __shared__ int s_seq[kRopeGroups];
     __shared__ int64_t s_pos[kRopeGroups];   // the token's place in its sequence

@@ -2,10 +2,14 @@
 
     python -m indexer_top_sparse_lightning_b200.profile_step --workload batch32 --steps 3
     python -m indexer_top_sparse_lightning_b200.profile_step --prolog decode32 --steps 3
+    python -m indexer_top_sparse_lightning_b200.profile_step --operator attn_batch32 --steps 3
 
 With --prolog, the indexer prolog runs instead (64 x 128 index heads, d_model
 7168, synthetic weights tile-packed once): decode32 = 32 sequences with one new
 token each, prefill4k / prefill16k = one sequence of 4096 / 16384 new tokens.
+
+With --operator, a case of perf/operators.py (prep_..., attn_..., weight_..., evict_...) runs
+instead: one call of an operator around the sparse attention per step.
 
 Each step is one dsa_decode call (indexer + Top-K + sparse attention).  The
 process exits non-zero if the device reports an error.  It prints the
@@ -57,14 +61,37 @@ def run_prolog(shape: str, steps: int) -> int:
     return 0 if st == 0 else 1
 
 
+def run_operator(name: str, steps: int) -> int:
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "perf", "operators.py")
+    spec = importlib.util.spec_from_file_location("operators", path)
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    state = ops.prepare({c["name"]: c for c in ops.listed()}[name], 1)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(steps + 1)]
+    ev[0].record()
+    for i in range(steps):
+        ops.run(state)
+        ev[i + 1].record()
+    torch.cuda.synchronize()
+    st = dsa.get_status(dsa.status_workspace())
+    print(" ".join(f"{ev[i].elapsed_time(ev[i + 1]) * 1e3:.1f}us" for i in range(steps)), f"status={st}")
+    return 0 if st == 0 else 1
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("--workload", default="batch32", choices=sorted(W.PRESETS))
     ap.add_argument("--steps", type=int, default=3)
     ap.add_argument("--indexer-only", action="store_true")
     ap.add_argument("--prolog", choices=sorted(PROLOG_SHAPES))
+    ap.add_argument("--operator", metavar="CASE")
     a = ap.parse_args(argv)
     dsa.load_library()
+    if a.operator:
+        return run_operator(a.operator, a.steps)
     if a.prolog:
         return run_prolog(a.prolog, a.steps)
     wl = W.preset(a.workload, with_kv=not a.indexer_only)
