@@ -413,7 +413,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  * q, cache formats and block tables are those of sparse_mla_attn.  Over an FP8
  * cache the scores are fp32 sums of the codes' products, times the scales (the 64
  * RoPE elements take part as values of 22 bits in units of their neighbours'
- * scale), and the output's values are rounded to fp16.
+ * scale), and the output's values are rounded to fp16.  Where max_q_per_seq new
+ * tokens make 4096 (token, head) rows or more, and batch x max_seq_len positions no
+ * more than 96 MiB of fp16 copy, the cache is copied into the scratch once (2304 bytes a
+ * position: two fp16 values per element and a factor per page, to 2^-22 of a value).
  * out device [T, H, 512] bf16; lse device [T, H] fp32 (natural log) or NULL.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * bf16 (fp16 over an FP8 cache) for the second product.

@@ -15,10 +15,19 @@ using namespace dsa::host;
 
 namespace {
 
-// Scratch: [headers][partial slots of the pairs].
+// An FP8 cache is copied as fp16 once per call, rather than converted in the kernel, when a
+// sequence can have this many tiles and the copy stays in L2.  (Us, copy / kernel, 128 heads:
+// one sequence of 16K positions with 16 new tokens 177 / 178, 64 456 / 572, 512 2857 / 4132, 2048
+// 10894 / 15592; 8 sequences of 16K to 131K, whose copy is 1.2 GB, 64 tokens 17864 / 16706, 2
+// tokens 899 / 548.)
+constexpr int64_t kCopyTiles = 32;
+constexpr int64_t kCopyBytes = int64_t(96) << 20;
+
+// Scratch: [headers][partial slots of the pairs][the fp16 copy, a factor per page].
 struct ChunkPlan {
     int pairs = 0;
-    size_t total = 0;
+    int64_t pages = 0;          // pages per sequence of the copy (0: none)
+    size_t copy_off = 0, scale_off = 0, total = 0;
 };
 
 dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevInfo& di, ChunkPlan& pl) {
@@ -37,6 +46,16 @@ dsa_status plan_chunk(const dsa_batch* bt, const dsa_attn_inputs* at, const DevI
     const int64_t blocks = tiles * (((int64_t)bt->max_seq_len + ChunkCfg::BLOCK - 1) / ChunkCfg::BLOCK);
     pl.pairs = (int)(blocks < pmax ? blocks : pmax);
     pl.total = align256(ChunkCfg::HEAD_BYTES + (size_t)pmax * 4 * (size_t)ChunkCfg::PART_BYTES);
+    if (at->kv_dtype == DSA_KV_FP8) {
+        const int64_t most = bt->max_q_per_seq < bt->num_tokens ? bt->max_q_per_seq : bt->num_tokens;
+        const int64_t pages = ((int64_t)bt->max_seq_len + kPage - 1) / kPage;
+        if (most * at->H >= kCopyTiles * ChunkCfg::ROWS && pages * bt->batch <= kCopyBytes / (kPage * kCopyRow * 2)) {
+            pl.pages = pages;
+            pl.copy_off = pl.total;
+            pl.scale_off = pl.copy_off + (size_t)pages * bt->batch * kPage * kCopyRow * 2;
+            pl.total = align256(pl.scale_off + (size_t)pages * bt->batch * 4);
+        }
+    }
     return DSA_OK;
 }
 
@@ -71,14 +90,16 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     p.H = at->H;
     p.max_blocks = batch->max_blocks_per_seq;
     p.num_blocks = batch->num_blocks;
-    const int64_t room = (int64_t)batch->max_blocks_per_seq * kPage;
+    p.staged = (int32_t)pl.pages;
+    const int64_t room = (pl.pages ? pl.pages : (int64_t)batch->max_blocks_per_seq) * kPage;
     p.max_len = (int32_t)(room < kMaxLen ? room : kMaxLen);
     p.tokens = p.max_tokens = INT32_MAX;
     p.scale_log2 = at->sm_scale * 1.4426950408889634f;
-    const bool fp8 = at->kv_dtype == DSA_KV_FP8;
+    const ChunkCache cache = at->kv_dtype != DSA_KV_FP8 ? kCacheBf16 : pl.pages ? kCacheCopy : kCacheFp8;
     CUtensorMap tm_q, tm_k, tm_v, tm_r;
-    bool maps = rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, kDqk, 64, ChunkCfg::KCH);
-    if (fp8) {
+    bool maps = rows_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->q, (uint64_t)batch->num_tokens * at->H, kDqk, 64,
+                         ChunkCfg::KCH);
+    if (cache == kCacheFp8) {
         p.codes = static_cast<const uint8_t*>(at->kv_cache);
         p.kv_scale = at->kv_scale;
         const uint64_t dims[2] = {(uint64_t)kDqk, (uint64_t)batch->num_blocks * kPage}, stride = kDqk;
@@ -88,14 +109,26 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
         };
         maps = maps && code_map(&tm_k, bk) && code_map(&tm_r, br) && code_map(&tm_v, bv);
     } else {
-        const uint64_t nrows = (uint64_t)batch->num_blocks * kPage;
-        maps = maps && rows_map(&tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->kv_cache, nrows, kDqk, 64, 3) &&
-               rows_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at->kv_cache, nrows, kDqk, 32, 4);
+        const void* rows = at->kv_cache;
+        uint64_t nrows = (uint64_t)batch->num_blocks * kPage;
+        if (cache == kCacheCopy) {
+            float* factors = reinterpret_cast<float*>(p.part + pl.scale_off);
+            if (dsa_status st = copy_fp8_pages(batch, at, pl.pages, p.part + pl.copy_off, factors, s)) return st;
+            p.page_scale = factors;
+            rows = p.part + pl.copy_off;
+            nrows = (uint64_t)pl.pages * batch->batch * kPage;
+        }
+        const CUtensorMapDataType type =
+            cache == kCacheCopy ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const uint64_t row = cache == kCacheCopy ? kCopyRow : kDqk;
+        maps = maps && rows_map(&tm_k, type, rows, nrows, row, 64, 3) && rows_map(&tm_v, type, rows, nrows, row, 32, 4);
     }
-    if (!fp8) tm_r = tm_k;         // not used
+    if (cache != kCacheFp8) tm_r = tm_k;         // not used
     if (!maps)
         return fail(DSA_ERR_CUDA, "tensor map encoding failed");
-    const auto kernel = fp8 ? &chunk_attn_kernel<true> : &chunk_attn_kernel<false>;
+    const auto kernel = cache == kCacheFp8    ? &chunk_attn_kernel<kCacheFp8>
+                        : cache == kCacheCopy ? &chunk_attn_kernel<kCacheCopy>
+                                              : &chunk_attn_kernel<kCacheBf16>;
     if (cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(kernel), ChunkCfg::SMEM))
         return fail(DSA_ERR_CUDA, "shared memory attribute", e);
     cudaLaunchAttribute attr[2];
@@ -108,7 +141,7 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(2 * pl.pairs, 1, 1);
-    cfg.blockDim = dim3(32 * ChunkCfg::warps(fp8), 1, 1);
+    cfg.blockDim = dim3(32 * ChunkCfg::warps(cache == kCacheFp8), 1, 1);
     cfg.dynamicSmemBytes = ChunkCfg::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;

@@ -66,22 +66,26 @@
 
 namespace dsa {
 
-// FP8: the cache holds e4m3 codes, which chunk_fp8.cuh brings to fp16 operands, and Q is
-// brought to fp16 in shared memory: both operands of an MMA have one type, and bf16
-// would round the products of codes and scales eight times as far.  A power of two per
-// row of Q keeps it in fp16's range.  The scores are put together from four accumulators
-// here; with t_s = S_s + log2 F_s (F_s the page's power of two) the weights that multiply
-// the values code * f / F are P_s F_s = 2^(t_s - m), so the reference m follows t, and the
-// sums of weights are those of 2^(t_s - m) / F_s.
-template <bool FP8>
-__global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
+// An FP8 cache (e4m3 codes) meets fp16 operands, and Q is brought to fp16 in shared memory:
+// both operands of an MMA have one type, and bf16 would round the products of codes and
+// scales eight times as far.  A power of two per row of Q keeps it in fp16's range.  The
+// operands are made by chunk_fp8.cuh, which leaves four score accumulators to be put together
+// here, or read from the fp16 copy of latent.cu (many tiles over few positions: the copy stays
+// in L2, and a code is converted once), whose rows hold the rounded values and what their
+// rounding left out: the scores take both, with twice the score MMAs and key loads.  With
+// t_s = S_s + log2 F_s (F_s the page's power of two) the weights that multiply the values
+// code * f / F are P_s F_s = 2^(t_s - m), so the reference m follows t, and the sums of
+// weights are those of 2^(t_s - m) / F_s.
+template <ChunkCache CACHE>
+__global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CUtensorMap tm_r) {
     using Cfg = ChunkCfg;
+    constexpr bool FP8 = CACHE == kCacheFp8, COPY = CACHE == kCacheCopy, F16 = CACHE != kCacheBf16;
     constexpr int SMW = Cfg::SOFTMAX_WARPS, QK_WARP = SMW, PV_WARP = SMW + 1;
     constexpr int KEY_WARP = SMW + 2, VALUE_WARP = SMW + 3, FIX_WARP = SMW + 5;
-    constexpr int KLOAD_WARP = SMW + 3, VLOAD_WARP = SMW + 4, FACTOR_WARP = SMW + 5;                 // FP8 (two factor warps)
+    constexpr int KLOAD_WARP = SMW + 3, FACTOR_WARP = SMW + 5;   // FP8: two loading warps, two of factors
     constexpr int FKEY_WARP = SMW + 8, FVALUE_WARP = FKEY_WARP + Cfg::CONV_WARPS;
     constexpr int SEG_WARP = FP8 ? SMW + 2 : SMW + 4;
     extern __shared__ uint8_t smem_raw[];
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
             mbar_init(&m->v_empty[i], FP8 ? 2 : 1);
             mbar_init(&m->v_land[i], 1);
         }
-        mbar_init(&m->q_full, FP8 ? 2 * SMW : 2);
+        mbar_init(&m->q_full, F16 ? 2 * SMW : 2);
         mbar_init(&m->q_land, 1);
         mbar_init(&m->q_empty, 1);
         for (int i = 0; i < 4; ++i) {
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                     ok = false;
                     break;
                 }
-                if constexpr (FP8) {
+                if constexpr (F16) {
                     mbar_arrive_expect_tx(&m->q_land, Cfg::Q_BYTES);
                     tma_load_3d(s_q, &tm_q, &m->q_land, 0, sg.row0 + 64 * (int)crank, 0);
                 } else {
@@ -250,7 +254,10 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
         const uint32_t k_lead = mapa_shared(smem_u32(&m->k_full[0]), 0), v_lead = mapa_shared(smem_u32(&m->v_full[0]), 0);
         TileRun sg = {};
         const int32_t* table = nullptr;
-        auto page_id = [&](int page) -> int { return chunk_page(p, sg, table, page); };
+        auto page_id = [&](int page) -> int {
+            const int id = chunk_page(p, sg, table, page);
+            return COPY && id >= 0 ? sg.b * p.staged + page : id;
+        };
         auto load_keys = [&](int id0, int id1) -> bool {
             const int id = crank == 0 ? id0 : id1;
             // a page that nobody sees is not loaded: its scores are replaced whatever they are
@@ -258,12 +265,15 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
             const bool mine = el && id >= 0;
             const int y = id * kPage;
 #pragma unroll 1
-            for (int g = 0; g < Cfg::KRING; ++g) {
-                if (!elected_wait(el, &m->k_empty[g], ph, abort, wlim)) return false;
-                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[g], bytes);
-                if (mine) tma_load_3d_pair(s_k + g * Cfg::KGROUP, &tm_k, k_lead + 8 * g, 0, y, 3 * g);
+            for (int g = 0; g < (COPY ? 2 : 1) * Cfg::KRING; ++g) {
+                const int kr = g % Cfg::KRING;
+                if (!elected_wait(el, &m->k_empty[kr], ph, abort, wlim)) return false;
+                if (crank == 0 && el) mbar_arrive_expect_tx(&m->k_full[kr], bytes);
+                // (the copy's small rests first, so that adding them up costs no bits of the sum)
+                const int chunk = !COPY ? 3 * g : g < Cfg::KRING ? 3 * g + 9 : 3 * g - 9;
+                if (mine) tma_load_3d_pair(s_k + kr * Cfg::KGROUP, &tm_k, k_lead + 8 * kr, 0, y, chunk);
+                if (kr == Cfg::KRING - 1) ph ^= 1;
             }
-            ph ^= 1;
             return true;
         };
         auto next_group = [&]() {
@@ -391,7 +401,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                     const int pos = k * Cfg::BLOCK + 32 * g + lane;
                     bool zero = pos >= sg.see;
                     if (!zero && pos >= sg.see_all) {
-                        constexpr uint32_t EXP = 0x7F80u;
+                        constexpr uint32_t EXP = F16 ? 0x7C00u : 0x7F80u;
                         uint32_t odd = 0;  // an exponent of all ones
 #pragma unroll 1
                         for (int q = 0; q < 32; ++q) {
@@ -459,7 +469,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                         for (int j = 0; j < 8; ++j)
                             if (el)
                                 umma_bf16_2cta(d, qd + ((j >> 2) * step + (j & 3) * 2), kd + ((j >> 2) * 512 + (j & 3) * 2),
-                                               Cfg::idesc_qk(FP8), j != 0 || g == 1);
+                                               Cfg::idesc_qk(F16), j != 0 || g == 1);
                         if (el) umma_commit_2cta(&m->k_empty[r], 3);
                         if (el && g > 0) umma_commit_2cta(&m->s_full[tile], 3);
                         if (++r == Cfg::KRING) {
@@ -473,18 +483,19 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                     tc_fence_after();
                     const uint32_t d = tm_s + (blk & 1) * 64;
 #pragma unroll 1
-                    for (int g = 0; g < Cfg::KRING; ++g) {
-                        if (!elected_wait(el, &m->k_full[g], ph, abort, wlim)) return false;
-                        const uint32_t base = g * (Cfg::KGROUP / 16);   // of Q's chunks as well: 8192 bytes each
+                    for (int g = 0; g < (COPY ? 2 : 1) * Cfg::KRING; ++g) {
+                        const int kr = g % Cfg::KRING;
+                        if (!elected_wait(el, &m->k_full[kr], ph, abort, wlim)) return false;
+                        const uint32_t base = kr * (Cfg::KGROUP / 16);   // of Q's chunks as well: 8192 bytes each
 #pragma unroll
                         for (int j = 0; j < 12; ++j)
                             if (el) {
                                 const uint32_t off = base + (j >> 2) * 512 + (j & 3) * 2;
-                                umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::idesc_qk(FP8), (g | j) != 0);
+                                umma_bf16_2cta(d, q_desc + off, k_desc + off, Cfg::idesc_qk(F16), (g | j) != 0);
                             }
-                        if (el) umma_commit_2cta(&m->k_empty[g], 3);
+                        if (el) umma_commit_2cta(&m->k_empty[kr], 3);
+                        if (kr == Cfg::KRING - 1) ph ^= 1;
                     }
-                    ph ^= 1;
                     if (el) umma_commit_2cta(&m->s_full[blk & 1], 3);
                 }
                 if (last && el) umma_commit_2cta(&m->q_empty, 3);
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                         for (int s16 = 0; s16 < 2; ++s16)
                             if (el)        // A = P [64 rows x 16 positions] K-major
                                 umma_bf16_2cta(tm_o + h * 128, pd + ((g >> 1) * 512 + (g & 1) * 4 + s16 * 2),
-                                               vd + (h * 512 + s16 * 128), Cfg::idesc_pv(FP8), g > 0 || s16 > 0 || !first);
+                                               vd + (h * 512 + s16 * 128), Cfg::idesc_pv(F16), g > 0 || s16 > 0 || !first);
                     if (el) umma_commit_2cta(&m->v_empty[r], 3);
                     if (++r == (FP8 ? Cfg::FVRING : Cfg::VRING)) {
                         r = 0;
@@ -594,7 +605,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
             const int32_t* table = p.block_table + (int64_t)sg.b * p.max_blocks;
             auto page_ok = [&](int k) -> bool { return FP8 || chunk_page(p, sg, table, 2 * k + half) != -2; };
             float c_row = p.scale_log2;                  // scores in log2 units
-            if constexpr (FP8) {
+            if constexpr (F16) {
                 ok = warp_wait(&m->q_land, ns & 1, abort, wlim);
                 ok = named_bar_and(1, SMT, ok);
                 if (!ok) break;
@@ -642,13 +653,23 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                 __syncwarp();
                 if (lane == 0) arrive_leader(&m->q_full, crank);
             }
+            // (the copy) the factor of this thread's page, one block ahead
+            auto page_factor = [&](int k, float old) -> float {
+                const int page = 2 * k + half;
+                return page * kPage < sg.see ? __ldg(p.page_scale + (int64_t)sg.b * p.staged + page) : old;
+            };
             bool next_ok = page_ok(sg.k0);
+            float next_f = COPY ? page_factor(sg.k0, 1.0f) : 1.0f;
             float mrun = -INFINITY, lrun = 0.0f, lfull = 0.0f;
             for (int k = sg.k0; k < sg.k1; ++k, ++blk) {
                 const uint32_t b = FP8 ? 0u : blk & 1, u = (FP8 ? blk : blk >> 1) & 1;
                 bool this_ok = next_ok;
                 const ChunkScales& rec = s_rec[blk % Cfg::NREC];
-                if (k + 1 < sg.k1) next_ok = page_ok(k + 1);
+                const float fk = next_f;
+                if (k + 1 < sg.k1) {
+                    next_ok = page_ok(k + 1);
+                    if (COPY) next_f = page_factor(k + 1, fk);
+                }
                 bool got = ok && (FP8 ? warp_wait(&m->rec_full[blk % Cfg::NREC], (blk / Cfg::NREC) & 1, abort, wlim)
                                       : warp_wait(&m->s_full[b], u, abort, wlim));
                 float2 sv[NP / 2];
@@ -692,8 +713,15 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                         __syncwarp();
                         if (lane == 0) arrive_leader(&m->s_empty[b], crank);
 #pragma unroll
-                        for (int i = 0; i < NP; i += 2)
-                            sv[i / 2] = mul_f32x2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), make_float2(c_row, c_row));
+                        for (int i = 0; i < NP; i += 2) {
+                            const float2 x = make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+                            if constexpr (COPY) {
+                                const float c = c_row * fk, l = log2_of_power(fk);
+                                sv[i / 2] = fma_f32x2(x, make_float2(c, c), make_float2(l, l));
+                            } else {
+                                sv[i / 2] = mul_f32x2(x, make_float2(c_row, c_row));
+                            }
+                        }
                     } else {
                         const float2 l2 = make_float2(rec.log2f[half], rec.log2f[half]);
 #pragma unroll
@@ -714,15 +742,15 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                 // (one barrier, no exchange); otherwise every row takes its new maximum.
                 float muse = mrun;
                 bool rescale = false;
-                if (!named_bar_and(1, SMT, ok && got && !(mx > mrun + Cfg::lazy(FP8)))) {
+                if (!named_bar_and(1, SMT, ok && got && !(mx > mrun + Cfg::lazy(F16)))) {
                     ok = named_bar_and(1, SMT, ok && got);
                     if (!ok) break;
                     float of[2 * PARTS], mnew = -INFINITY;
                     exchange(mx, of);
 #pragma unroll
                     for (int i = 0; i < 2 * PARTS; ++i) mnew = fmaxf(mnew, of[i]);
-                    rescale = mnew > mrun + Cfg::lazy(FP8);      // identical in the threads of a row
-                    if (rescale) muse = mnew - Cfg::drop(FP8);
+                    rescale = mnew > mrun + Cfg::lazy(F16);      // identical in the threads of a row
+                    if (rescale) muse = mnew - Cfg::drop(F16);
                 }
                 const float base = muse == -INFINITY ? 0.0f : muse;   // (nothing seen yet: 2^-inf)
                 uint32_t pk[NP / 2];
@@ -735,7 +763,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                     // roundings cancel in part); lse takes the sum before rounding.  fp16 weights
                     // divide by that one as well: divided by a small F, the rounding of a
                     // weight that is subnormal in fp16 would count in the sum as it does not in O.
-                    if constexpr (FP8) {
+                    if constexpr (F16) {
                         const __half2 h = __floats2half2_rn(e.x, e.y);
                         pk[i] = *reinterpret_cast<const uint32_t*>(&h);
                     } else {
@@ -745,6 +773,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                     full = add_f32x2(full, e);
                 }
                 float sum = full.x + full.y;
+                if constexpr (COPY) sum /= fk;
                 if constexpr (FP8) {
                     sum *= rec.inv[half];
                     __syncwarp();
@@ -774,7 +803,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
                     }
                 }
                 lfull = fmaf(lfull, f, sum);
-                lrun = FP8 ? lfull : fmaf(lrun, f, rounded.x + rounded.y);
+                lrun = F16 ? lfull : fmaf(lrun, f, rounded.x + rounded.y);
                 mrun = muse;
                 if (ok) {
                     // P row hl, chunk of this half: 16-byte pieces of a 128-byte row (128-byte swizzle)
@@ -795,7 +824,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(FP8), 1)
             const bool ofull = ok && warp_wait(&m->o_full, ns & 1, abort, wlim);
             ok = named_bar_and(1, SMT, ofull);
             if (!ok) break;
-            const float ltot = row_sum(lrun), lft = FP8 ? ltot : row_sum(lfull);
+            const float ltot = row_sum(lrun), lft = F16 ? ltot : row_sum(lfull);
             tc_fence_after();
             const bool empty = ltot == 0.0f;   // the row saw nothing here
             const int64_t row = (int64_t)sg.row0 + rr;

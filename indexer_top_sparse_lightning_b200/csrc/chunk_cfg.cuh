@@ -8,12 +8,16 @@
 
 namespace dsa {
 
+// Where keys and values come from: bf16 rows; e4m3 codes, converted in the kernel; the fp16
+// copy of an FP8 cache.
+enum ChunkCache { kCacheBf16, kCacheFp8, kCacheCopy };
+
 struct ChunkCfg {
     static constexpr int ROWS = 128;                    // (token, head) rows of a tile
     static constexpr int BLOCK = 128;                   // positions of a block (two pages)
     static constexpr int KCH = 9;                       // 64-column chunks of a latent row
     static constexpr int KRING = 3;                     // groups of keys that are kept
-    static constexpr int KGROUP = 3 * 8192;             // bf16: 64 rows x 3 chunks, three make a block
+    static constexpr int KGROUP = 3 * 8192;             // 64 rows x 3 chunks; three make a block, six over the fp16 copy
     static constexpr int VGROUPS = 4;                   // groups of a block's values: 32 rows x 4 chunks (this CTA's)
     static constexpr int VRING = 3;                     // groups that are kept
     static constexpr int VGROUP = 4 * 4096;
@@ -50,14 +54,14 @@ struct ChunkCfg {
     // replacement waits for the P.V in flight.  fp16 weights end at 2^16 and lose bits below
     // 2^-14: references seven below the maximum keep them in [2^-14, 2^15] down to 2^-21 of the
     // largest weight, and to 2^-32 of it with an absolute error.
-    static constexpr float lazy(bool fp8) { return fp8 ? 15.0f : 32.0f; }
-    static constexpr float drop(bool fp8) { return fp8 ? 7.0f : 0.0f; }
+    static constexpr float lazy(bool fp16) { return fp16 ? 15.0f : 32.0f; }
+    static constexpr float drop(bool fp16) { return fp16 ? 7.0f : 0.0f; }
     static constexpr int NSEG = 4;                      // segment ring
     static constexpr int TMEM_COLS = 512;               // O: [0, 256); from column 256 two score buffers of 64, or (FP8) one of 4 x 64
     // fp16 operands: the bf16 descriptor without its two operand-format bits
     static constexpr uint32_t BF16_BITS = (1u << 7) | (1u << 10);
-    static constexpr uint32_t idesc_qk(bool fp8) { return idesc_bf16_f32(128, BLOCK, false, false) & ~(fp8 ? BF16_BITS : 0u); }
-    static constexpr uint32_t idesc_pv(bool fp8) { return idesc_bf16_f32(128, 256, false, true) & ~(fp8 ? BF16_BITS : 0u); }
+    static constexpr uint32_t idesc_qk(bool fp16) { return idesc_bf16_f32(128, BLOCK, false, false) & ~(fp16 ? BF16_BITS : 0u); }
+    static constexpr uint32_t idesc_pv(bool fp16) { return idesc_bf16_f32(128, 256, false, true) & ~(fp16 ? BF16_BITS : 0u); }
     // partial result of (pair, side, CTA): O [64 rows][512] fp32, then (m, sum, sum for lse, -) per row.
     // Side 1: the pair holds the tile's first blocks; side 0: later ones.
     static constexpr int64_t PART_O = 64 * 512 * 4;
@@ -80,6 +84,7 @@ struct ChunkParams : ListParams {
     uint32_t* status;         // status word; words 1-2 hold the test hooks
     const uint8_t* codes;     // FP8: [num_blocks * 64, 576] e4m3 codes, [num_blocks * 64, 5] scales
     const float* kv_scale;
+    const float* page_scale;  // fp16 copy: the power-of-two factor of each page, [B, staged]
     float scale_log2;         // sm_scale * log2(e)
 };
 

@@ -6,9 +6,8 @@
 // shared-memory pipe is half busy with them, beside the MMAs' own reads (tensor pipes 24 %).
 // Two tokens of 8 sequences of 16K to 128K positions take 545 us, two tiles of 128 rows
 // over 530K positions; over an fp16 copy of the cache in global memory, which wrote and
-// read 2304 bytes a position, they took 900 with the copy.  Many tiles over one short
-// sequence favoured the copy, which then stayed in L2 (2048 tokens at 16K: 10.9 ms, here
-// 15.6); it was given up for its scratch, 2304 bytes for every position of the batch.
+// read 2304 bytes a position, they took 900 with the copy.  (Many tiles over positions whose copy
+// stays in L2 take the copy: chunk.cu.)
 //
 // Two teams of CONV_WARPS warps convert, one the keys and one the values, a ring group
 // (16 KB of fp16, 8 KB of codes) at a time; the codes of the groups behind are on their way to

@@ -1,4 +1,4 @@
-// latent.cu -- copies that the attention weights read in place of an FP8 latent cache:
+// latent.cu -- copies that the dense kernels read in place of an FP8 latent cache:
 // the sequences' rows, and queries, as fp16; and the tensor maps over rows.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -19,8 +19,8 @@ namespace dsa {
 // largest value that the page's scales allow below 2^14; positions behind the
 // sequence's end do not count, whatever they hold.  One block per page: its 64 rows
 // are 2304 runs of 16 codes, nine per thread, all loaded before any is converted.
-// Memory-bound: reads 596 bytes a row and writes 2304.  (Dense attention converts in its own
-// kernel, chunk_fp8.cuh; the attention weights read this copy.)
+// Memory-bound: reads 596 bytes a row and writes 2304.  (Dense attention of few new tokens
+// converts in its own kernel instead, chunk_fp8.cuh.)
 struct PagesParams {
     const int32_t* seq_lens;
     const int32_t* block_table;

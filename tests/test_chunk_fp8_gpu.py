@@ -182,3 +182,20 @@ def test_timeout_is_reported_and_recoverable():
     assert dsa.get_status(ws) == 5                     # DSA_ERR_TIMEOUT
     ws.reset()
     assert torch.equal(clean, call()) and dsa.get_status(ws) == 0
+
+
+def test_copied_and_converted_agree():
+    # 40 tokens of 128 heads over few positions are copied, one by one they are converted in the
+    # kernel: each within its bound of the same sum
+    n, H = 40, 128
+    pg = Paged([900], [n], seed=12)
+    q = randn(31, n, H, ROW, scale=3.0)
+    codes, scale, val = cache(pg, 32)
+    ref = reference(pg, q, lambda b: val[pg.rows(b)], fp16=True)
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    check(pg, out, lse, ref)
+    for j in (0, 17, n - 1):
+        one = Paged([900], [n], seed=12)
+        one.lens, one.nq, one.cu, one.real = np.array([900 - n + j + 1]), np.array([1]), np.array([0, 1], np.int32), 1
+        o, x = run(one, q[j:j + 1], codes, kv_scale=scale.cuda())
+        check(one, o, x, [r[j:j + 1] for r in ref])
