@@ -17,7 +17,7 @@
 //
 // Longer sequences (kEvictWide positions and more) take the same steps with a group of up to
 // all SMs' CTAs each (evict_wide_kernel), joined through histograms and counts in
-// scratch: eight CTAs would need 270 us for a million positions, most of it histogram
+// scratch; a range's keys stay in shared memory where they fit: eight CTAs would need 270 us for a million positions, most of it histogram
 // adds, which a CTA takes one by one.
 //
 // evict_copy_kernel: memory-bound, every kept row read and written once.  A block
@@ -42,6 +42,7 @@ static_assert(kEvictWarps == 32, "one lane per warp in the sums over warps");
 constexpr int kEvictBins = 2048;
 constexpr int kEvictWide = 65537;           // longest sequence from which the wide kernels are used
 constexpr int kEvictWideRange = 4096;       // positions per CTA there, at least
+constexpr int kEvictWideKeys = 9216;        // keys of a CTA there that shared memory holds
 constexpr int kEvictMaxArrays = 8;
 constexpr int kEvictCopyThreads = 256;
 constexpr int kEvictCopyRows = 32;
@@ -308,10 +309,10 @@ __device__ __forceinline__ bool evict_group_barrier(const EvictParams& p, EvictS
 
 // Long sequences: a group of CTAs each, all groups at once (a cooperative launch), a group's
 // sequences one after another.  The steps are those of the cluster kernel, joined through
-// histograms and counts in scratch and a barrier of the group; a CTA's keys are read
-// again in every step (they stay in L2).
+// histograms and counts in scratch and a barrier of the group.
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __grid_constant__ EvictParams p) {
     __shared__ EvictShared s_all;
+    __shared__ uint32_t s_key[kEvictWideKeys];
     EvictShared* s = &s_all;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = (int)blockIdx.x / p.ctas, cta = (int)blockIdx.x % p.ctas;
@@ -334,7 +335,11 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __gr
         const int lo = lo64 < L ? (int)lo64 : L;
         const int n = L - lo < per ? L - lo : per;
         const float* w = p.weight + (int64_t)b * p.stride + lo;
+        // the keys of a range that fits stay in shared memory after the first step
+        const bool fits = n <= kEvictWideKeys;
+        bool kept = false;
         auto key_at = [&](int i) -> uint32_t {
+            if (kept) return s_key[i];
             const float x = __ldg(w + i);
             const int pos = lo + i;
             if (pos < p.sink || pos >= L - p.recent) return 0xFFFFFFFFu;
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __gr
         };
         uint32_t prefix = 0, need = (uint32_t)keep;
 #pragma unroll 1
-        for (int d = 0; d < 3; ++d) {
+        for (int d = 0; d < 3; ++d, kept = fits) {
             const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
             const uint32_t mask = d == 2 ? 1023u : 2047u;
             const uint32_t above_mask = d == 0 ? 0u : d == 1 ? 0xFFE00000u : 0xFFFFFC00u;
@@ -359,7 +364,9 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_wide_kernel(const __gr
                 }
 #pragma unroll
                 for (int u = 0; u < BATCH; ++u) {
-                    const bool here = i0 + u * kEvictThreads + (int)threadIdx.x < n && (k[u] & above_mask) == prefix;
+                    const int i = i0 + u * kEvictThreads + (int)threadIdx.x;
+                    if (d == 0 && fits && i < n) s_key[i] = k[u];
+                    const bool here = i < n && (k[u] & above_mask) == prefix;
                     zeros += __popc(__ballot_sync(0xffffffffu, here && k[u] == ZERO));
                     if (here && k[u] != ZERO) atomicAdd(&s->hist[(k[u] >> shift) & mask], 1u);
                 }
