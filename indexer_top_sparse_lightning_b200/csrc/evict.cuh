@@ -28,7 +28,7 @@
 //
 // Measured: 32 sequences of 28K to 32K cut to 8192 positions, latent rows and index keys,
 // 147 us: 24 to choose, 122 to copy 740 MB (6.07 TB/s).  A million positions cut to 65536, FP8 rows:
-// 61 us, about half each for the choice and the copy.
+// 55 us, about half each for the choice and the copy.
 #pragma once
 #include "common.h"
 #include "paging.cuh"
