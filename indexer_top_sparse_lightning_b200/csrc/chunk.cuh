@@ -119,11 +119,9 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
         mbar_init(&m->q_full, F16 ? 2 * SMW : 2);
         mbar_init(&m->q_land, 1);
         mbar_init(&m->q_empty, 1);
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&m->s_full[i], 1);
             mbar_init(&m->s_empty[i], 2 * SMW);   // those of both CTAs
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(&m->p_full[i], 2 * SMW);
             mbar_init(&m->p_empty[i], 1);
             mbar_init(&m->drain[i], 1);
@@ -455,9 +453,9 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
 #pragma unroll 1
                     for (int g = 0; g < 5; ++g) {
                         const int tile = g < 2 ? 3 : g - 2;
-                        // this accumulator's scores of the block before have been read
-                        if (g != 1) {
-                            if (!elected_wait(el, &m->s_empty[tile], (blk & 1) ^ 1, abort, wlim)) return false;
+                        // the block before's scores have been read: of accumulator 3, of the others
+                        if (g == 0 || g == 2) {
+                            if (!elected_wait(el, &m->s_empty[g >> 1], (blk & 1) ^ 1, abort, wlim)) return false;
                             tc_fence_after();
                         }
                         if (!elected_wait(el, &m->k_full[r], ph, abort, wlim)) return false;
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
                                 umma_bf16_2cta(d, qd + ((j >> 2) * step + (j & 3) * 2), kd + ((j >> 2) * 512 + (j & 3) * 2),
                                                Cfg::idesc_qk(F16), j != 0 || g == 1);
                         if (el) umma_commit_2cta(&m->k_empty[r], 3);
-                        if (el && g > 0) umma_commit_2cta(&m->s_full[tile], 3);
+                        if (el && (g == 1 || g == 4)) umma_commit_2cta(&m->s_full[g >> 2], 3);
                         if (++r == Cfg::KRING) {
                             r = 0;
                             ph ^= 1;
@@ -675,22 +673,24 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
                 float2 sv[NP / 2];
                 float mx = -INFINITY;
                 if constexpr (FP8) {
-                    // the accumulators in the order in which they are made: 3, 0, 1, 2
+                    // the accumulators in the order in which they are made: 3, then 0, 1 and 2
                     this_ok = rec.ok[half] != 0;
 #pragma unroll
                     for (int i = 0; i < NP / 2; ++i) sv[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
                     for (int i4 = 0; got && i4 < 4; ++i4) {
                         const int t = (i4 + 3) & 3;
-                        got = warp_wait(&m->s_full[t], blk & 1, abort, wlim);
+                        if (i4 < 2) got = warp_wait(&m->s_full[i4], blk & 1, abort, wlim);
                         if (got) {
                             uint32_t a[NP];
                             tc_fence_after();
                             tmem_ld32(tm_s + lane_off + 64 * t + NP * part, a);
                             tmem_wait_ld();
                             tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_leader(&m->s_empty[t], crank);
+                            if (i4 == 0 || i4 == 3) {
+                                __syncwarp();
+                                if (lane == 0) arrive_leader(&m->s_empty[i4 == 3], crank);
+                            }
                             const float4* f4 = reinterpret_cast<const float4*>(&rec.f[t][p0]);
 #pragma unroll
                             for (int i = 0; i < NP; i += 4) {

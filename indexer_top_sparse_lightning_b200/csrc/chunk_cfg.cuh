@@ -100,7 +100,7 @@ struct ChunkMisc {
     uint64_t rec_full[ChunkCfg::NREC], rec_empty[ChunkCfg::NREC];   // (FP8) position factors
     uint64_t kc_empty[ChunkCfg::KRING], vc_empty[ChunkCfg::FVRING]; // (FP8) codes have been converted
     uint64_t q_empty;
-    uint64_t s_full[4], s_empty[4];       // per score buffer; FP8: per accumulator
+    uint64_t s_full[2], s_empty[2];       // per score buffer; FP8: of accumulator 3, of the others
     uint64_t p_full[2], p_empty[2];
     uint64_t o_full, o_empty, drain[2];
     uint64_t seg_full[ChunkCfg::NSEG], seg_empty[ChunkCfg::NSEG];
