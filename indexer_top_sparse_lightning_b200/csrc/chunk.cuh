@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
         for (int i = 0; i < Cfg::KRING; ++i) {
             mbar_init(&m->k_full[i], FP8 ? 2 : 1);    // CTA 0's loader, for both CTAs; FP8: both CTAs' converters
             mbar_init(&m->k_empty[i], FP8 ? 2 : 1);
-            mbar_init(&m->kc_empty[i], 1);
         }
         for (int i = 0; i < Cfg::VRING; ++i) {
             mbar_init(&m->v_full[i], FP8 ? 2 : 1);    // ... or fixer
@@ -139,7 +138,10 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
         }
         if (FP8) {
             // the operand rings are empty: no MMAs to wait for in their first round
-            for (int i = 0; i < Cfg::KRING; ++i) mbar_arrive(&m->k_empty[i]);
+            for (int i = 0; i < Cfg::FKRING; ++i) {
+                mbar_init(&m->kc_empty[i], 1);
+                mbar_arrive(&m->k_empty[i]);
+            }
             for (int i = 0; i < Cfg::FVRING; ++i) {
                 mbar_init(&m->vc_empty[i], 1);
                 mbar_arrive(&m->v_empty[i]);
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
                                                Cfg::idesc_qk(F16), j != 0 || g == 1);
                         if (el) umma_commit_2cta(&m->k_empty[r], 3);
                         if (el && (g == 1 || g == 4)) umma_commit_2cta(&m->s_full[g >> 2], 3);
-                        if (++r == Cfg::KRING) {
+                        if (++r == Cfg::FKRING) {
                             r = 0;
                             ph ^= 1;
                         }

@@ -25,7 +25,7 @@ struct ChunkCfg {
     // x 4 chunks), and groups of codes on their way there
     static constexpr int FGROUP = 16384;
     static constexpr int CGROUP = 8192;
-    static constexpr int FVRING = 2;
+    static constexpr int FKRING = 2, FVRING = 3;        // (three and two: 536 us for 524)
     static constexpr int TILES = 5;                     // scales of a position
     static constexpr int NREC = 3;                      // blocks whose position factors are kept
     static constexpr int CONV_WARPS = 4;                // warps that convert keys, and as many for values
@@ -38,9 +38,9 @@ struct ChunkCfg {
     static constexpr int OFF_XM = OFF_V + VRING * VGROUP;   // exchange between the threads of a row
     // FP8: one weight buffer, keys, values, codes of keys and of values, position factors
     static constexpr int OFF_FK = OFF_P + P_BYTES;
-    static constexpr int OFF_FV = OFF_FK + KRING * FGROUP;
+    static constexpr int OFF_FV = OFF_FK + FKRING * FGROUP;
     static constexpr int OFF_KC = OFF_FV + FVRING * FGROUP;
-    static constexpr int OFF_VC = OFF_KC + KRING * CGROUP;
+    static constexpr int OFF_VC = OFF_KC + FKRING * CGROUP;
     static constexpr int OFF_REC = OFF_VC + FVRING * CGROUP;
     static constexpr int OFF_MISC = OFF_XM + 256 * 4;
     static constexpr int MISC_BYTES = 1024;
@@ -98,7 +98,7 @@ struct ChunkMisc {
     uint64_t q_full;                      // (CTA 0) Q of both CTAs
     uint64_t q_land;                      // (FP8) this CTA's Q, still bf16
     uint64_t rec_full[ChunkCfg::NREC], rec_empty[ChunkCfg::NREC];   // (FP8) position factors
-    uint64_t kc_empty[ChunkCfg::KRING], vc_empty[ChunkCfg::FVRING]; // (FP8) codes have been converted
+    uint64_t kc_empty[ChunkCfg::FKRING], vc_empty[ChunkCfg::FVRING]; // (FP8) codes have been converted
     uint64_t q_empty;
     uint64_t s_full[2], s_empty[2];       // per score buffer; FP8: of accumulator 3, of the others
     uint64_t p_full[2], p_empty[2];
@@ -117,9 +117,9 @@ static_assert(sizeof(ChunkMisc) <= ChunkCfg::MISC_BYTES, "misc block exceeds its
 // FP8: the factors of a block's positions (both pages), for this CTA.
 struct ChunkScales {
     float f[4][ChunkCfg::BLOCK];          // of the four score accumulators
-    float last[ChunkCfg::BLOCK];          // the fifth tile's scale
     float log2f[2], inv[2];               // log2 F and 1 / F of the two pages
-    uint32_t value[2][ChunkCfg::BLOCK];   // f_t / F of this CTA's two tiles of values, as two fp16 parts
+    // f_t / F of this CTA's two tiles of values, as two fp16 parts (in the making: first the fifth tile's scale)
+    uint32_t value[2][ChunkCfg::BLOCK];
     uint2 key[kPage];                     // g3 and g4 of this CTA's page, as two fp16 parts each
     int ok[2];                            // the two pages' ids are good
     int pad[2];

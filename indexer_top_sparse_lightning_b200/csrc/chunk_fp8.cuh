@@ -4,7 +4,7 @@
 // What bounds it: instructions and shared memory.  A block's 70 KB of codes per CTA become 144
 // KB of operands; the converting and softmax warps issue in 61 % of the cycles and the
 // shared-memory pipe is half busy with them, beside the MMAs' own reads (tensor pipes 24 %).
-// Two tokens of 8 sequences of 16K to 128K positions take 545 us, two tiles of 128 rows
+// Two tokens of 8 sequences of 16K to 128K positions take 524 us, two tiles of 128 rows
 // over 530K positions; over an fp16 copy of the cache in global memory, which wrote and
 // read 2304 bytes a position, they took 900 with the copy.  (Many tiles over positions whose copy
 // stays in L2 take the copy: chunk.cu.)
@@ -86,7 +86,7 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
                         rec.f[t][pos] = raw[i][t];
                         if (seen) top = fmaxf(top, fabsf(raw[i][t]));
                     }
-                    rec.last[pos] = raw[i][4];
+                    rec.value[0][pos] = __float_as_uint(raw[i][4]);
                 }
                 // magnitudes compare as integers
                 const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
@@ -110,7 +110,7 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
             if (k < sg.k0) continue;
 #pragma unroll 1
             for (int pos = 64 * half + lane; pos < 64 * half + 64; pos += 32) {
-                const float f3 = rec.f[3][pos], f4 = rec.last[pos];
+                const float f3 = rec.f[3][pos], f4 = __uint_as_float(rec.value[0][pos]);
                 float u = f3, g3 = 1.0f, num = f4, den = f3;
                 const bool large = fabsf(f4) > 64.0f * fabsf(f3);
                 if (large) {
@@ -179,7 +179,7 @@ __device__ __forceinline__ bool fp8_codes(const ChunkParams& p, ChunkMisc* m, ui
     uint8_t* codes = smem + (keys ? Cfg::OFF_KC : Cfg::OFF_VC);
     uint64_t* full = keys ? m->k_empty : m->v_empty;
     uint64_t* empty = keys ? m->kc_empty : m->vc_empty;
-    const uint32_t slots = keys ? Cfg::KRING : Cfg::FVRING;
+    const uint32_t slots = keys ? Cfg::FKRING : Cfg::FVRING;
     uint32_t cr = 0, ph = 1;
 #pragma unroll 1
     for (int ns = 0;; ++ns) {
@@ -301,7 +301,7 @@ __device__ __forceinline__ bool fp8_keys(const ChunkParams& p, ChunkMisc* m, uin
                     mbar_arrive(&m->kc_empty[r]);
                     if (g == 1) mbar_arrive(&m->rec_empty[rr]);
                 }
-                if (++r == Cfg::KRING) {
+                if (++r == Cfg::FKRING) {
                     r = 0;
                     ph ^= 1;
                 }
