@@ -151,7 +151,7 @@ dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs* at, voi
     if (pl.pairs < 2) return DSA_OK;
     cudaLaunchConfig_t ccfg;
     memset(&ccfg, 0, sizeof ccfg);
-    ccfg.gridDim = dim3(2 * di.sms, 1, 1);
+    ccfg.gridDim = dim3(di.sms, 1, 1);
     ccfg.blockDim = dim3(ChunkCfg::COMBINE_THREADS, 1, 1);
     ccfg.stream = s;
     ccfg.attrs = attr;

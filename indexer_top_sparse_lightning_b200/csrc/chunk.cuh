@@ -40,7 +40,7 @@
 // of 128 heads sits at the ridge of HBM and tensor rate.  The last 2048 tokens of a
 // 16K prompt take 7.15 ms, 1.22 PFLOP/s (cuBLAS holds 1.38 for as long; the clock is at the power
 // limit); 32 tokens over 32K positions each 340 us, 3.6 TB/s and 0.86 PFLOP/s at once;
-// one token at 4K 17.8 us, most of it start, planning and merge.
+// one token at 4K 16.6 us, most of it start, planning and merge.
 //
 // Masked positions.  Scores past a row's own position are replaced, not
 // multiplied.  In P.V a weight of zero still multiplies the value row, so rows
@@ -892,17 +892,21 @@ __global__ void __launch_bounds__(32 * ChunkCfg::warps(CACHE == kCacheFp8), 1)
 // units), l_s and e_s its sums of weights,
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,
 //   lse = (M + log2 sum_s 2^(m_s - M) e_s) ln 2,  M = max m_s,
-// added up in split order.  The rows of all such tiles form one list (a scan over
+// added up in a fixed order.  The rows of all such tiles form one list (a scan over
 // the pairs' headers), shared out evenly; four warps take a row, 128 columns each,
-// with eight splits' loads in flight per lane (a tile of few rows may have as many
-// splits as there are pairs, and waiting for them one by one took 22 us).
-__global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kernel(const __grid_constant__ ChunkParams p,
-                                                                                  int np) {
+// with eight splits' loads in flight per lane.  Where there is a block for every row,
+// all of its warps take that row, a quarter of the splits each, joined in shared memory (a
+// tile of few rows may have as many splits as there are pairs, and waiting for them
+// one by one took 22 us; with four warps a row one token of 16 heads at 4K took 17.4 us, at
+// 8K 25.5, one of 128 heads at 16K 34.8; with a block a row 16.6, 18.6 and 26.2).
+__global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS, 1) chunk_combine_kernel(const __grid_constant__ ChunkParams p,
+                                                                                     int np) {
     using Cfg = ChunkCfg;
-    constexpr int ROWS = Cfg::COMBINE_THREADS / 128;     // rows a block takes at a time
+    constexpr int QUARTERS = Cfg::COMBINE_THREADS / 128;
     __shared__ int s_first[Cfg::MAX_PAIRS + 1];          // rows of the pairs before
     __shared__ int4 s_head[Cfg::MAX_PAIRS];
     __shared__ int s_sum[Cfg::COMBINE_THREADS / 32];
+    __shared__ float4 s_acc[QUARTERS][128];
     griddep_wait();
     const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
     int4 h = make_int4(0, 0, 0, 0);
@@ -926,7 +930,9 @@ __global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kerne
     __syncthreads();
     const int rows = s_first[Cfg::MAX_PAIRS];
     constexpr int PER = Cfg::MAX_PAIRS / 32;
-    for (int i = (int)blockIdx.x * ROWS + warp / 4; i < rows; i += (int)gridDim.x * ROWS) {
+    const bool whole = rows <= (int)gridDim.x;           // a block takes a row
+    const int per = whole ? 1 : QUARTERS, quarter = warp / 4;
+    for (int i = (int)blockIdx.x * per + (whole ? 0 : quarter); i < rows; i += (int)gridDim.x * per) {
         int lo = 0, hi = Cfg::MAX_PAIRS - 1;             // the pair whose rows hold i
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kerne
 #pragma unroll
         for (int j = 0; j < PER; ++j)
 #pragma unroll 1
-            for (int g = 0; g < 32 && 32 * j + g < S; g += 8) {
+            for (int g = whole ? 8 * quarter : 0; g < 32 && 32 * j + g < S; g += whole ? 8 * QUARTERS : 8) {
                 float4 v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -984,6 +990,20 @@ __global__ void __launch_bounds__(ChunkCfg::COMBINE_THREADS) chunk_combine_kerne
                     }
                 }
             }
+        if (whole) {
+            __syncthreads();                             // (the row before has been read)
+            s_acc[quarter][32 * (warp & 3) + lane] = acc;
+            __syncthreads();
+            if (quarter > 0) continue;
+#pragma unroll
+            for (int q = 1; q < QUARTERS; ++q) {
+                const float4 o = s_acc[q][32 * (warp & 3) + lane];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
+            }
+        }
         const bool empty = l == 0.0f;
         const float inv = empty ? 0.0f : 1.0f / l;
         *reinterpret_cast<uint2*>(p.out + out_row * kDv + col) =

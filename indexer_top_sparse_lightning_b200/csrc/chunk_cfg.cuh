@@ -68,7 +68,7 @@ struct ChunkCfg {
     static constexpr int64_t PART_BYTES = PART_O + 64 * 16;
     static constexpr int64_t HEAD_BYTES = 2048;         // one int4 per pair: the tile that starts there and ends in a later pair
     static constexpr int MAX_PAIRS = 128;                // the merge keeps four splits per lane
-    static constexpr int COMBINE_THREADS = 256;         // at least MAX_PAIRS
+    static constexpr int COMBINE_THREADS = 512;         // at least MAX_PAIRS
 };
 static_assert(ChunkCfg::SMEM <= 232448, "shared memory exceeds the per-CTA limit");
 static_assert(ChunkCfg::OFF_P % 1024 == 0 && ChunkCfg::OFF_K % 1024 == 0 && ChunkCfg::OFF_V % 1024 == 0, "swizzled operands need 1024-byte alignment");
