@@ -34,6 +34,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -159,22 +160,23 @@ def load_library():
     lib.indexer_prolog_pack.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_void_p]
     lib.indexer_prolog_pack.restype = ctypes.c_int
-    lib.dsa_qk_norm_rope.argtypes = [P(_Batch), P(_Rope), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+    # (argument blocks of these are packed bytes, or structures by reference)
+    lib.dsa_qk_norm_rope.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_void_p]
     lib.dsa_qk_norm_rope.restype = ctypes.c_int
-    lib.dsa_chunk_scratch_size.argtypes = [P(_Batch), P(_Attn)]
+    lib.dsa_chunk_scratch_size.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.dsa_chunk_scratch_size.restype = ctypes.c_size_t
-    lib.dsa_chunk_attn.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+    lib.dsa_chunk_attn.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_chunk_attn.restype = ctypes.c_int
-    lib.dsa_weight_scratch_size.argtypes = [P(_Batch), P(_Attn)]
+    lib.dsa_weight_scratch_size.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.dsa_weight_scratch_size.restype = ctypes.c_size_t
-    lib.dsa_attn_weight.argtypes = [P(_Batch), P(_Attn), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
+    lib.dsa_attn_weight.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_attn_weight.restype = ctypes.c_int
-    lib.dsa_evict_scratch_size.argtypes = [P(_Batch)]
+    lib.dsa_evict_scratch_size.argtypes = [ctypes.c_void_p]
     lib.dsa_evict_scratch_size.restype = ctypes.c_size_t
-    lib.dsa_cache_evict.argtypes = [P(_Batch), P(_Evict), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+    lib.dsa_cache_evict.argtypes = [ctypes.c_void_p, P(_Evict), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_size_t, ctypes.c_void_p]
     lib.dsa_cache_evict.restype = ctypes.c_int
     lib.dsa_status_str.argtypes = [ctypes.c_int32]
@@ -579,6 +581,17 @@ def _dense(t, name, dtype, shape, dev: int) -> int:
     raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
 
 
+def _packer(struct_type):
+    """pack() of a ctypes structure's fields, in their order: a third of the time of an instance."""
+    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    packed = struct.Struct("@" + "".join(code[t] for _, t in struct_type._fields_) + "0P")
+    assert packed.size == ctypes.sizeof(struct_type)
+    return packed.pack
+
+
+_pack_batch, _pack_rope, _pack_attn = _packer(_Batch), _packer(_Rope), _packer(_Attn)
+
+
 def _vector(t, name, dtype, dev: int):
     """(pointer, length) of a dense vector."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.get_device() == dev >= 0 \
@@ -588,16 +601,16 @@ def _vector(t, name, dtype, dev: int):
     raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
 
 
-def _batch_struct(batch: Batch, T: int, dev: int) -> _Batch:
-    """The batch's argument block, its tensors checked."""
+def _batch_args(batch: Batch, T: int, dev: int):
+    """(argument block, number of sequences) of a batch, its tensors checked."""
     i32, table = torch.int32, batch.block_table
     lens, B = _vector(batch.seq_lens, "seq_lens", i32, dev)
     cu, n = _vector(batch.cu_q, "cu_q", i32, dev)
     if n != B + 1:
         raise ValueError(f"cu_q dim 0 must be {B + 1}, got {n}")
     W = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else None
-    return _Batch(B, T, lens, cu, _dense(table, "block_table", i32, (B, W), dev), W, batch.num_blocks,
-                  batch.max_seq_len, batch.max_q_per_seq)
+    tp = _dense(table, "block_table", i32, (B, W), dev)
+    return _pack_batch(B, T, lens, cu, tp, W, batch.num_blocks, batch.max_seq_len, batch.max_q_per_seq), B
 
 
 def _rows(t, name, ndim: int, dev: int):
@@ -641,7 +654,7 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
     f32 = torch.float32
     H = qp = kp = cp = sp = qn = kn = R = 0
     qs, ks, kt = (0, 0), (0,), KV_BF16
-    qg = kg = fp = pp = None
+    qg = kg = fp = pp = 0
     if q is not None:
         qp, (T, H, D), qs = _rows(q, "q", 3, dev)
     if k is not None:
@@ -664,9 +677,9 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
         R *= 2
     if positions is not None:
         pp = _dense(positions, "positions", torch.int32, (T,), dev)
-    cb = _batch_struct(batch, T, dev)
-    s = _Rope(qp, qs[0], qs[1], kp, ks[0], H, D, qg, kg, qn, kn, eps, fp, R,
-              D - R if rope_off is None else rope_off, bool(interleaved), pp, kt)
+    cb, _ = _batch_args(batch, T, dev)
+    s = _pack_rope(qp, qs[0], qs[1], kp, ks[0], H, D, qg, kg, qn, kn, eps, fp, R,
+                   D - R if rope_off is None else rope_off, bool(interleaved), pp, kt)
     with _On(dev, stream) as on:
         status = _status(workspace, dev)
         op = 0
@@ -678,7 +691,7 @@ def dsa_qk_norm_rope(batch: Batch, inv_freq, q=None, k=None, *, q_gamma=None, k_
                 op = _dense(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
                 if op == qp and not q.is_contiguous():
                     raise ValueError("q_out may be q only when q is contiguous")
-        rc = lib.dsa_qk_norm_rope(ctypes.byref(cb), ctypes.byref(s), op, cp, sp, status, on)
+        rc = lib.dsa_qk_norm_rope(cb, s, op, cp, sp, status, on)
     if rc != 0:
         raise DsaError(rc, "dsa_qk_norm_rope")
     return q_out if q is not None else None
@@ -692,12 +705,12 @@ def _latent_attn(q, kv_cache, sm_scale, kv_scale, num_blocks: int):
     dev = q.get_device()
     qp = _dense(q, "q", torch.bfloat16, (T, H, 576), dev)
     if kv_scale is None:
-        kt, sp = KV_BF16, None
+        kt, sp = KV_BF16, 0
         cp = _dense(kv_cache, "kv_cache", torch.bfloat16, (num_blocks, 64, 576), dev)
     else:
         kt, sp = KV_FP8, _dense(kv_scale, "kv_scale", torch.float32, (num_blocks, 64, 5), dev)
         cp = _dense(kv_cache, "kv_cache", torch.uint8, (num_blocks, 64, 576), dev)
-    return _Attn(qp, cp, H, sm_scale, kt, sp), T, H, dev
+    return _pack_attn(qp, cp, H, sm_scale, kt, sp), T, H, dev
 
 
 def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None, out=None, lse=None,
@@ -708,10 +721,10 @@ def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None,
     call's stream; the status word is that of `workspace` (status_workspace() by default)."""
     lib = load_library()
     at, T, H, dev = _latent_attn(q, kv_cache, sm_scale, kv_scale, batch.num_blocks)
-    cb = _batch_struct(batch, T, dev)
+    cb, _ = _batch_args(batch, T, dev)
     with _On(dev, stream) as on:
         status = _status(workspace, dev)
-        need = lib.dsa_chunk_scratch_size(ctypes.byref(cb), ctypes.byref(at))
+        need = lib.dsa_chunk_scratch_size(cb, at)
         if need == 0:
             raise DsaError(2, "dsa_chunk_scratch_size")
         if out is None:
@@ -725,7 +738,7 @@ def dsa_chunk_attn(batch: Batch, q, kv_cache, sm_scale: float, *, kv_scale=None,
         else:
             lp = None if lse is None else _dense(lse, "lse", torch.float32, (T, H), dev)
         scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
-        rc = lib.dsa_chunk_attn(ctypes.byref(cb), ctypes.byref(at), op, lp, status, scratch.data_ptr(), need, on)
+        rc = lib.dsa_chunk_attn(cb, at, op, lp, status, scratch.data_ptr(), need, on)
     if rc != 0:
         raise DsaError(rc, "dsa_chunk_attn")
     return out, lse
@@ -738,17 +751,17 @@ def dsa_attn_weight(batch: Batch, q, kv_cache, sm_scale: float, lse, weight, *, 
     [T, H] is the attention's.  Returns weight."""
     lib = load_library()
     at, T, H, dev = _latent_attn(q, kv_cache, sm_scale, kv_scale, batch.num_blocks)
-    cb = _batch_struct(batch, T, dev)
+    cb, B = _batch_args(batch, T, dev)
     lp = _dense(lse, "lse", torch.float32, (T, H), dev)
     n = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 2 else None
-    wp = _dense(weight, "weight", torch.float32, (cb.batch, n), dev)
+    wp = _dense(weight, "weight", torch.float32, (B, n), dev)
     with _On(dev, stream) as on:
         status = _status(workspace, dev)
-        need = lib.dsa_weight_scratch_size(ctypes.byref(cb), ctypes.byref(at))
+        need = lib.dsa_weight_scratch_size(cb, at)
         if need == 0:
             raise DsaError(2, "dsa_weight_scratch_size")
         scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
-        rc = lib.dsa_attn_weight(ctypes.byref(cb), ctypes.byref(at), lp, wp, n, decay, status, scratch.data_ptr(), need, on)
+        rc = lib.dsa_attn_weight(cb, at, lp, wp, n, decay, status, scratch.data_ptr(), need, on)
     if rc != 0:
         raise DsaError(rc, "dsa_attn_weight")
     return weight
@@ -765,8 +778,7 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
     lib = load_library()
     dev = weight.get_device() if isinstance(weight, torch.Tensor) else -1
     n = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 2 else None
-    cb = _batch_struct(batch, max(1, batch.max_q_per_seq), dev)
-    B = cb.batch
+    cb, B = _batch_args(batch, max(1, batch.max_q_per_seq), dev)
     wp = _dense(weight, "weight", torch.float32, (B, n), dev)
     W = new_table.shape[1] if isinstance(new_table, torch.Tensor) and new_table.dim() == 2 else None
     tp = _dense(new_table, "new_table", torch.int32, (B, W), dev)
@@ -800,9 +812,9 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
             lp = out_len.data_ptr()
         else:
             lp = _dense(out_len, "out_len", torch.int32, (B,), dev)
-        need = lib.dsa_evict_scratch_size(ctypes.byref(cb))
+        need = lib.dsa_evict_scratch_size(cb)
         scratch = torch.empty(max(need, 256), dtype=torch.uint8, device=weight.device)
-        rc = lib.dsa_cache_evict(ctypes.byref(cb), ctypes.byref(s), ip, lp, status, scratch.data_ptr(), need, on)
+        rc = lib.dsa_cache_evict(cb, ctypes.byref(s), ip, lp, status, scratch.data_ptr(), need, on)
     if rc != 0:
         raise DsaError(rc, "dsa_cache_evict")
     return out_idx, out_len
