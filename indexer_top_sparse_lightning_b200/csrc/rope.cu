@@ -53,8 +53,18 @@ dsa_status check_rope(const dsa_batch* bt, const dsa_rope_inputs* in, const void
 
 template <int NV>
 cudaError_t launch(const RopeParams& p, int64_t blocks, cudaStream_t s) {
-    qk_norm_rope_kernel<NV><<<(unsigned)blocks, kRopeThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    // (the kernel waits for the one before it ahead of its first read)
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(kRopeThreads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, &qk_norm_rope_kernel<NV>, p);
 }
 
 }  // namespace
