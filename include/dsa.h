@@ -412,8 +412,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  *     lse[t,h] = log sum_s exp(S[t,h,s])
  * q, cache formats and block tables are those of sparse_mla_attn.  Over an FP8
  * cache the scores are fp32 sums of the codes' products, times the scales (the 64
- * RoPE elements take part as values of 22 bits in units of their neighbours'
- * scale), and the output's values are rounded to fp16.  Where max_q_per_seq new
+ * RoPE elements take part as two fp16 values each: to 2^-21 of themselves or 2^-31 of the
+ * scale before theirs, whichever is more; where their scale is more than 2^22 times that
+ * one, the elements before them are rounded to 2^-31 of theirs), and the output's values
+ * are rounded to fp16.  Where max_q_per_seq new
  * tokens make 4096 (token, head) rows or more, and batch x max_seq_len positions no
  * more than 96 MiB of fp16 copy, the cache is copied into the scratch once (2304 bytes a
  * position: two fp16 values per element and a factor per page, to 2^-22 of a value).

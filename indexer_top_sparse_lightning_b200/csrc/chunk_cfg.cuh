@@ -120,7 +120,7 @@ struct ChunkScales {
     float log2f[2], inv[2];               // log2 F and 1 / F of the two pages
     // f_t / F of this CTA's two tiles of values, as two fp16 parts (in the making: first the fifth tile's scale)
     uint32_t value[2][ChunkCfg::BLOCK];
-    uint2 key[kPage];                     // g3 and g4 of this CTA's page, as two fp16 parts each
+    uint2 key[kPage];                     // g3 and g4 of this CTA's page, as two fp16 parts each (g4's rest kRestUp times)
     int ok[2];                            // the two pages' ids are good
     int pad[2];
 };

@@ -20,11 +20,15 @@
 //   S = f_0 S_0 + f_1 S_1 + f_2 S_2 + u S_3,
 // f_t the scale of tile t (128 elements) of the position, S_t its codes times Q in
 // fp32.  The fifth tile, 64 elements, has no accumulator of its own (tensor memory
-// is full) and joins S_3 as fp16 values code * g4 in two parts, the value rounded
-// (2^-11) and the rest, with u = f_3, g3 = 1, g4 = f_4 / f_3.  Where |f_4| > 64
-// |f_3|, fp16 would overflow: there u = f_4 / 64, g4 = 64, and tile 3's codes take
-// the factor g3 = f_3 / u, rounded to fp16 (a 2^-11 part of something 64 times
-// smaller than its neighbour).
+// is full) and joins S_3, in a unit u of the position's own:
+//   u S_3 = f_3 sum c_3 q + f_4 sum c_4 q,   u = f_3 2^j, g3 = f_3 / u = 2^-j, g4 = f_4 / u.
+// A scale says nothing of how large its tile's codes are (a tile of zeros has the scale 1), nor of
+// how large the queries are that they meet, so neither tile may lose bits to the other: c_3 g3 is
+// exact for -7 <= j <= 15 (a code has four bits, 2^-9 to 448; fp16 goes from 2^-24 to 65504), and c_4 g4
+// is taken as two fp16 parts, the value rounded and the rest, to 2^-21 of it or 2^-24 u, whichever
+// is more.  j is floor(log2 |f_4 / f_3|) - 6, which brings |g4| into [64, 128) (the products end below
+// 2^16), and -7 at least, where 2^-24 u is 2^-31 |f_3|.  Past |f_4| = 2^22 |f_3|, j is above 15 and
+// c_3 g3 is rounded, to 2^-25 u, which is at most 2^-31 |f_4|.
 //
 // Values: code * f_t / F, one rounding to fp16, with F the power of two that brings
 // the largest value scale of the page's positions into [64, 128), so that values end
@@ -38,10 +42,39 @@
 
 namespace dsa {
 
-// A value as two fp16 parts, the rounded value (low) and the rest.
-__device__ __forceinline__ uint32_t two_halves(float v) {
-    const __half h = __float2half_rn(v), l = __float2half_rn(v - __half2float(h));
+// A value as two fp16 parts, the rounded value (low) and the rest times `up`.
+__device__ __forceinline__ uint32_t two_halves(float v, float up = 1.0f) {
+    const __half h = __float2half_rn(v), l = __float2half_rn((v - __half2float(h)) * up);
     return (uint32_t)__half_as_ushort(h) | (uint32_t)__half_as_ushort(l) << 16;
+}
+// The rest of g4 is stored 2^10 times as large and meets codes 2^10 times as small (exact), so that it
+// does not lose bits to fp16's smallest step before it is multiplied by a code of up to 448.
+constexpr float kRestUp = 1024.0f;
+
+// The unit of tiles 3 and 4 of a position, and their scales in it.  Magnitudes compare as integers, and
+// their difference shifted by the mantissa's width is floor(log2 |f4 / f3|) of normal numbers.
+struct Fp8Unit {
+    float u, g3, g4;
+};
+__device__ __forceinline__ Fp8Unit fp8_unit(float f3, float f4) {
+    const int b3 = (int)(__float_as_uint(f3) & 0x7FFFFFFFu), b4 = (int)(__float_as_uint(f4) & 0x7FFFFFFFu);
+    Fp8Unit t;
+    constexpr int kTiny = 27 << 23;                      // 2^-100
+    if (b3 >= kTiny && b3 < 0x7F800000) {
+        const int d = ((b4 - b3) >> 23) - 6, j = d < -7 ? -7 : d;
+        t.u = __uint_as_float(__float_as_uint(f3) + ((uint32_t)j << 23));
+        t.g3 = j > 60 ? 0.0f : __uint_as_float((uint32_t)(127 - j) << 23);
+        t.g4 = f4 / t.u;
+    } else if (b3 < kTiny) {                             // nothing beside any f4 to be met
+        t.u = __uint_as_float((uint32_t)((b4 < kTiny ? kTiny : b4) - (6 << 23)) & 0x7F800000u);
+        t.g3 = f3 / t.u;
+        t.g4 = f4 / t.u;
+    } else {                                             // infinite or NaN: the score is, whatever the codes
+        t.u = f3;
+        t.g3 = 1.0f;
+        t.g4 = 0.0f;
+    }
+    return t;
 }
 
 // The factors of the positions of page `half` of every block: a warp each, two positions a lane.
@@ -111,17 +144,9 @@ __device__ __forceinline__ bool fp8_factors(const ChunkParams& p, ChunkMisc* m, 
 #pragma unroll 1
             for (int pos = 64 * half + lane; pos < 64 * half + 64; pos += 32) {
                 const float f3 = rec.f[3][pos], f4 = __uint_as_float(rec.value[0][pos]);
-                float u = f3, g3 = 1.0f, num = f4, den = f3;
-                const bool large = fabsf(f4) > 64.0f * fabsf(f3);
-                if (large) {
-                    u = f4 * 0.015625f;
-                    num = f3;
-                    den = u;
-                }
-                const float g = num != 0.0f ? num / den : 0.0f;
-                if (large) g3 = g;
-                rec.f[3][pos] = u;
-                if (half == (int)crank) rec.key[pos & (kPage - 1)] = make_uint2(two_halves(g3), two_halves(large ? 64.0f : g));
+                const Fp8Unit t = fp8_unit(f3, f4);
+                rec.f[3][pos] = t.u;
+                if (half == (int)crank) rec.key[pos & (kPage - 1)] = make_uint2(two_halves(t.g3, 1.0f), two_halves(t.g4, kRestUp));
                 rec.value[0][pos] = two_halves(rec.f[2 * crank][pos] * inv);
                 rec.value[1][pos] = two_halves((crank == 0 ? rec.f[1][pos] : f3) * inv);
             }
@@ -264,14 +289,14 @@ __device__ __forceinline__ bool fp8_keys(const ChunkParams& p, ChunkMisc* m, uin
 #pragma unroll 1
                         for (int j = 0; j < NR; ++j) {
                             const uint32_t f = rec.key[rrow + j * 8 * CW].y;
-                            const __half2 gh = low_half(f), gl = high_half(f);
+                            const __half2 gh = low_half(f), gl = high_half(f), down = __float2half2_rn(1.0f / kRestUp);
                             __half2 h[8], l[8];
                             widen16(ld_shared_v4(rsrc + off + j * (8 * CW * 64)), h);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const __half2 c = h[e];
                                 h[e] = __hmul2(c, gh);
-                                l[e] = __hfma2(c, gl, __hfma2(c, gh, __hneg2(h[e])));
+                                l[e] = __hfma2(__hmul2(c, down), gl, __hfma2(c, gh, __hneg2(h[e])));
                             }
                             put16(rdst + to + j * (8 * CW * 128), l);
                             put16(rdst + to + j * (8 * CW * 128) + 8192, h);

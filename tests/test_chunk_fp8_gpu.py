@@ -199,3 +199,66 @@ def test_copied_and_converted_agree():
         one.lens, one.nq, one.cu, one.real = np.array([900 - n + j + 1]), np.array([1]), np.array([0, 1], np.int32), 1
         o, x = run(one, q[j:j + 1], codes, kv_scale=scale.cuda())
         check(one, o, x, [r[j:j + 1] for r in ref])
+
+
+def _few(seed, T, H, where, k=4):
+    """Queries with k elements that are not zero in each of the ranges `where`: the fp32 sum of the score's
+    products has that many terms, so that what is off is the operands."""
+    r = np.random.default_rng(seed)
+    q = torch.zeros(T, H, ROW)
+    for t in range(T):
+        for h in range(H):
+            for lo, hi in where:
+                at = r.choice(np.arange(lo, hi), k, replace=False)
+                q[t, h, at] = torch.from_numpy(r.standard_normal(k).astype(np.float32) * 3)
+    return q
+
+
+@pytest.mark.parametrize("mag", [-10, -4, 0, 4, 10])
+@pytest.mark.parametrize("zero", [(512, 576), (384, 512), (448, 512), None])
+@pytest.mark.parametrize("ratio", [-12, 0, 12])
+def test_scores_of_neighbouring_tiles_are_exact(zero, mag, ratio):
+    # One position a sequence, so that lse is the score itself.  The RoPE tile is 2^ratio times the
+    # latents' size; a tile of zeros has the scale 1 beside neighbours of any size (mag).  The products of
+    # codes are exact in fp32 and 4 or 8 of them are added (8 half steps of 2^-24 of the sum of magnitudes,
+    # and as many for the four scales and the query's).  RoPE values c g4 take part as two fp16 parts: with
+    # g4 = gh + gl, h = c gh rounded and l = c gl + (c gh - h), |gl| <= 2^-11 g4 (off by 2^-22 g4) and
+    # |c gh - h| <= 2^-11 c g4, so l <= 2^-10 c g4 is off by 2^-21 c g4: 3 * 2^-22 in all, or by two half steps
+    # of 2^-24 where it is subnormal, in a unit that is at least a 128th of tile 3's scale (the unit is that or
+    # a 64th of the RoPE tile's, whose own 2^-21 covers it): 2^-31 of that scale.  The score in log2 units is put
+    # together with the page's exponent, |log2 F| <= 32: eight roundings of 1.45 |S| + 48.
+    B, H = 48, 8
+    pg = Paged([1] * B, [1] * B, seed=14)
+    x = randn(61, pg.num_blocks, PAGE, ROW).float() * 2.0 ** mag
+    x[..., 512:] *= 2.0 ** ratio
+    if zero:
+        x[..., zero[0]:zero[1]] = 0
+    codes, scale, val = fp8_rows(x.to(torch.bfloat16))
+    q = _few(62, B, H, [(384, 448), (512, ROW)]) * 2.0 ** -mag
+    q[..., 512:] *= 2.0 ** -ratio
+    q = q.to(torch.bfloat16)
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    rows = np.concatenate([pg.rows(b) for b in range(B)])
+    v, f = val.view(-1, ROW)[rows], scale.view(-1, 5)[rows].double()
+    s = torch.einsum("thd,td->th", q.double(), v) * SCALE
+    size = torch.einsum("thd,td->th", q.double().abs(), v.abs()) * SCALE
+    rope = torch.einsum("thd,td->th", q.double().abs()[..., 512:], v.abs()[:, 512:]) * SCALE
+    step = q.double().abs()[..., 512:].sum(-1) * f[:, 3:4] * 2.0 ** -31 * SCALE
+    tol = 16 * 2.0 ** -24 * size + 3 * 2.0 ** -22 * rope + step + 8 * 2.0 ** -24 * (1.45 * s.abs() + 48)
+    err = (lse.cpu().double() - s).abs()
+    assert (err <= tol).all(), f"worst {float((err / tol).max()):.1f} of the bound, off by {float(err.max()):.2e}"
+
+
+@pytest.mark.parametrize("mag", [-6, 0, 6])
+@pytest.mark.parametrize("zero", [(512, 576), (384, 512), (384, 576), (0, 128), (0, 576)])
+@pytest.mark.parametrize("n", [20, 130])          # converted in the kernel; copied
+def test_tiles_of_zeros(n, zero, mag):
+    # some rows have tiles of zeros, which have the scale 1, between others of any size
+    H = 32
+    pg = Paged([700, 130], [3, n], seed=15)
+    x = randn(63, pg.num_blocks, PAGE, ROW).float() * 2.0 ** mag
+    x[:, ::3, zero[0]:zero[1]] = 0
+    codes, scale, val = fp8_rows(x.to(torch.bfloat16))
+    q = (randn(64, pg.T, H, ROW, scale=3.0).float() * 2.0 ** -mag).to(torch.bfloat16)
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
