@@ -426,7 +426,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  * and do not reach its result.  Rows of out and lse behind the last sequence
  * (t >= cu_q[B]) are left as they were.  Sequences without new tokens are
  * allowed.  A page id out of range, or lengths that do not fit the table, are
- * recorded as DSA_ERR_DEVICE_BOUNDS; the positions of such a page are not seen.
+ * recorded as DSA_ERR_DEVICE_BOUNDS; the positions of such a page are not seen, and such a
+ * length is taken as the table's.  A length below the sequence's count of new tokens is
+ * recorded too: tokens at p_t < 0 see nothing, and their rows of out and lse are left as
+ * they were.  So is a cu_q past num_tokens; the rows that are there keep their positions.
  *
  * status: a status area (256 bytes, zero-filled before its first use; the start
  * of any workspace of this library serves), read by dsa_get_status; calls may
@@ -461,7 +464,8 @@ DSA_API dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs*
  * power-of-two factor per page: 2^-22 of a value), which then holds max_seq_len
  * rows of 2304 bytes for each sequence.
  * More than max_q_per_seq new tokens of a sequence, or a length above max_seq_len,
- * are recorded as DSA_ERR_DEVICE_BOUNDS (the surplus is not counted).
+ * are recorded as DSA_ERR_DEVICE_BOUNDS (the surplus is not counted); so is a
+ * length below the count of new tokens (tokens at p_t < 0 add nothing).
  * scratch: dsa_weight_scratch_size bytes, 256-byte aligned, of any contents, one
  * each for calls that may overlap in time.  The sums are added in a fixed order:
  * equal calls give equal bits.  Errors as for dsa_chunk_attn.

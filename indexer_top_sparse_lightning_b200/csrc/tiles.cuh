@@ -109,23 +109,22 @@ struct TileList {
         return (i + 1 < s.tiles ? (i + 1 + s.first) / (G * H) : (s.c + s.n - 1) / BLOCK) + 1;
     }
 
-    // Sequence b, with sizes that no input can push out of range: tokens past T are
-    // dropped, a length is cut to max_len (both reported by `ok`).
+    // Sequence b, with sizes that no input can push out of range: a length is cut to max_len, tokens in
+    // front of position 0 (a length below their number) and tokens past T are left out, all reported by
+    // `ok`.  Token j of nq stands at len - nq + j whatever is left out.
     static __device__ __forceinline__ ChunkSeq seq(const ListParams& p, int b, bool& ok) {
         ChunkSeq s;
-        int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-        const int len = __ldg(p.seq_lens + b);
-        ok = q0 >= 0 && q1 >= q0 && q1 <= p.T && len <= p.max_len && (q1 == q0 || len >= q1 - q0) &&
-             q1 - q0 <= p.max_tokens;
-        q0 = q0 < 0 ? 0 : q0 > p.T ? p.T : q0;
-        q1 = q1 < q0 ? q0 : q1 > p.T ? p.T : q1;
-        int n = q1 - q0;
+        const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), len = __ldg(p.seq_lens + b);
+        const int64_t nq = q1 > q0 ? (int64_t)q1 - q0 : 0;
+        ok = q0 >= 0 && q1 >= q0 && q1 <= p.T && len <= p.max_len && (q1 == q0 || len >= nq) && nq <= p.max_tokens;
         s.len = len < 0 ? 0 : len > p.max_len ? p.max_len : len;
-        if (s.len < n) n = s.len;             // a sequence shorter than its new tokens: the rest sees nothing
-        s.c = s.len - n + p.tok0;
+        const int64_t first = (int64_t)q1 - (nq < s.len ? nq : s.len);      // the token at position 0 or the first one
+        const int lo = first < 0 ? 0 : first > p.T ? p.T : (int)first, hi = q1 < lo ? lo : q1 > p.T ? p.T : q1;
+        const int n = hi - lo;
+        s.c = s.len - (int)(q1 - (int64_t)lo) + p.tok0;
         s.n = n - p.tok0 < p.tokens ? n - p.tok0 : p.tokens;
         if (s.n < 0) s.n = 0;
-        s.row0 = (q0 + p.tok0) * p.H;
+        s.row0 = (lo + p.tok0) * p.H;
         s.rows = s.n * p.H;
         s.tiles = (s.rows + ROWS - 1) / ROWS;
         const int64_t ch = (int64_t)s.c * p.H;

@@ -341,3 +341,45 @@ def test_timeout_is_reported_and_recoverable():
     ws.reset()
     again, _ = dsa.dsa_chunk_attn(pg.batch(), q, kv, SCALE, workspace=ws)
     assert dsa.get_status(ws) == 0 and torch.equal(clean, again)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_length_below_the_new_tokens_is_reported(fp8):
+    # token j stands at seq_lens - nq + j: the first tokens of such a sequence stand in front of its start and
+    # see nothing, their rows stay as they were; the others are attended to as ever
+    n, L, H = 90, 70, 24
+    pg = Paged([300, n, 64], [5, n, 1], seed=12)
+    q = randn(41, pg.T, H, ROW, scale=3.0)
+    kv, kw = latent(pg, 42, nan_elsewhere=False), {}
+    if fp8:
+        kv, scale, val = fp8_rows(kv)
+        kw = dict(kv_scale=scale.cuda())
+    else:
+        val = kv
+    pg.lens[1] = L
+    ws = dsa.Workspace()
+    out = torch.full((pg.T, H, DV), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((pg.T, H), 5.0, device="cuda")
+    dsa.dsa_chunk_attn(pg.batch(), q.cuda(), kv.cuda(), SCALE, out=out, lse=lse, workspace=ws, **kw)
+    assert dsa.get_status(ws) == 6
+    cut = Paged([300, n, 64], [5, n, 1], seed=12)              # the tokens that stand in the sequence
+    cut.lens[1], cut.nq[1] = L, L
+    cut.cu = np.array([0, 5, 5 + L, 6 + L], np.int32)
+    cut.real = cut.T = 6 + L
+    keep = torch.tensor([t for t in range(pg.T) if not 5 <= t < 5 + n - L])
+    check(cut, out[keep.cuda()], lse[keep.cuda()],
+          reference(cut, q[keep], lambda b: val.view(-1, ROW)[cut.rows(b)], fp16=fp8))
+    assert (out[5:5 + n - L] == 5).all() and (lse[5:5 + n - L] == 5).all()
+
+
+def test_more_new_tokens_than_rows_are_reported():
+    # a cu_q that goes past the queries: the rows that are there keep their tokens' positions
+    lens, nq, H, gone = [300, 400, 64], [5, 90, 3], 24, 50
+    pg = Paged(lens, nq, seed=13)
+    q, kv = randn(51, pg.T, H, ROW, scale=3.0), latent(pg, 52)
+    ref = [r[:pg.T - gone] for r in reference(pg, q, lambda b: kv.view(-1, ROW)[pg.rows(b)])]
+    ws = dsa.Workspace()
+    out, lse = dsa.dsa_chunk_attn(pg.batch(), q[:pg.T - gone].cuda(), kv.cuda(), SCALE, workspace=ws)
+    assert dsa.get_status(ws) == 6
+    pg.real = pg.T - gone
+    check(pg, out, lse, ref)

@@ -224,3 +224,37 @@ def test_rows_that_saw_nothing_add_nothing(nq, H):
     a, b = (dsa.dsa_attn_weight(pg.batch(), x, kv, SCALE, lse, torch.zeros(2, 700, device="cuda")) for x in (clean, dirty))
     assert_status_ok()
     assert torch.equal(a, b) and float(a.sum()) > 0
+
+
+@pytest.mark.parametrize("n,L,H", [(90, 70, 24), (4, 3, 16)])
+def test_a_length_below_the_new_tokens_is_reported(n, L, H):
+    # the tokens in front of the sequence's start (token j stands at seq_lens - nq + j) add nothing
+    pg = Paged([300, n, 64], [5, n, 1], seed=12)
+    q, kv = randn(81, pg.T, H, ROW, scale=3.0), latent(pg, 82, nan_elsewhere=False)
+    pg.lens[1] = L
+    ws, w = dsa.Workspace(), torch.zeros(3, 300, device="cuda")
+    lse = torch.full((pg.T, H), 3.0)
+    cut = Paged([300, n, 64], [5, n, 1], seed=12)
+    cut.lens[1], cut.nq[1] = L, L
+    cut.cu = np.array([0, 5, 5 + L, 6 + L], np.int32)
+    cut.real = cut.T = 6 + L
+    keep = torch.tensor([t for t in range(pg.T) if not 5 <= t < 5 + n - L])
+    dsa.dsa_attn_weight(pg.batch(), q.cuda(), kv.cuda(), SCALE, lse.cuda(), w, workspace=ws)
+    assert dsa.get_status(ws) == 6
+    val, bound = expect(cut, q[keep], lambda b: kv.view(-1, ROW)[cut.rows(b)], lse[keep], torch.zeros(3, 300), 1.0)
+    assert ((w.double() - val).abs() <= bound).all()
+
+
+def test_more_new_tokens_than_rows_are_reported():
+    # a cu_q that goes past the queries: the rows that are there keep their tokens' positions
+    gone, H = 50, 24
+    pg = Paged([300, 400, 64], [5, 90, 3], seed=13)
+    q, kv = randn(91, pg.T, H, ROW, scale=3.0), latent(pg, 92)
+    n = pg.T - gone
+    ws, w = dsa.Workspace(), torch.zeros(3, 400, device="cuda")
+    lse = torch.full((pg.T, H), 3.0)
+    dsa.dsa_attn_weight(pg.batch(), q[:n].cuda(), kv.cuda(), SCALE, lse[:n].cuda(), w, workspace=ws)
+    assert dsa.get_status(ws) == 6
+    lse[n:] = -math.inf                                  # rows that are not there add nothing
+    val, bound = expect(pg, q, lambda b: kv.view(-1, ROW)[pg.rows(b)], lse, torch.zeros(3, 400), 1.0)
+    assert ((w.double() - val).abs() <= bound).all()
