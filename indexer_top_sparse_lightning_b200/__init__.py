@@ -35,6 +35,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -517,6 +518,7 @@ def indexer_prolog(batch: Batch, x, w_proj, k_gamma, eps: float, k_cache, k_scal
 
 
 _status_ws = {}
+_status_lock = threading.Lock()
 
 
 def status_workspace(device=None) -> Workspace:
@@ -529,11 +531,14 @@ def status_workspace(device=None) -> Workspace:
     if key not in _status_ws:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the default status area is not there yet: call status_workspace() before the capture")
-        ws = Workspace(torch.device("cuda", key))
-        ws.get(256)
-        # zeroed before any stream can use it
-        torch.cuda.synchronize(ws.device)
-        _status_ws[key] = ws
+        with _status_lock:
+            # (another thread may have been first: the area that it was given stays)
+            if key not in _status_ws:
+                ws = Workspace(torch.device("cuda", key))
+                ws.get(256)
+                # zeroed before any stream can use it
+                torch.cuda.synchronize(ws.device)
+                _status_ws[key] = ws
     return _status_ws[key]
 
 

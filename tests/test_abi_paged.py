@@ -175,3 +175,33 @@ def test_cache_evict_rejects_counts_that_32_bits_would_wrap():
 
 def test_rope_rejects_an_unaligned_status(lib):
     assert _call_rope(lib, status=2) == INVALID
+
+
+def test_first_calls_of_two_threads_share_one_status_area(monkeypatch):
+    # kernels and captured graphs hold its address: the area that a thread was given must be the one that stays
+    import threading
+    import time
+
+    import torch
+
+    class Area:
+        def __init__(self, device):
+            self.device = device
+
+        def get(self, n):
+            time.sleep(0.05)
+
+    monkeypatch.setattr(dsa, "_status_ws", {})
+    monkeypatch.setattr(dsa, "Workspace", Area)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: time.sleep(0.05))
+    start, got = threading.Barrier(4), []
+
+    def first():
+        start.wait()
+        got.append(dsa.status_workspace(0))
+
+    threads = [threading.Thread(target=first) for _ in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len({id(w) for w in got}) == 1 and dsa.status_workspace(0) is got[0]
