@@ -630,10 +630,13 @@ def _rows(t, name, ndim: int, dev: int):
         if t.dim() != ndim:
             raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
         raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
-    shape, strides, p = t.shape, t.stride(), t.data_ptr()
-    if not t.is_contiguous():
+    shape, p = t.shape, t.data_ptr()
+    if t.is_contiguous():
+        # (not t.stride(): that of a dimension of one element may be anything)
+        strides = (shape[1] * shape[2], shape[2], 1) if ndim == 3 else (shape[1], 1)
+    else:
         # the stride of a dimension of one element is never used
-        strides = [s if n > 1 else 0 for n, s in zip(shape, strides)]
+        strides = [s if n > 1 else 0 for n, s in zip(shape, t.stride())]
         if (shape[-1] > 1 and strides[-1] != 1) or any(s % 8 for s in strides[:-1]):
             raise ValueError(f"{name} needs dense rows 16 bytes apart, got strides {t.stride()}")
     if p % 16:

@@ -217,3 +217,42 @@ def test_captured_and_on_another_stream():
     graph.replay()
     assert_status_ok()
     assert torch.equal(out, ref * 2) and torch.equal(cache, want)
+
+
+@pytest.mark.parametrize("T,H", [(1, 6), (5, 1), (1, 1)])
+def test_strides_that_are_never_used_may_be_any(T, H):
+    # one token, or one head: the stride of a dimension of one element is not used
+    pg = Paged([90], [T], seed=6)
+    D = 128
+    wide = randn(81, T, H * D + D + 4).cuda()                  # rows 4 elements off a 16-byte boundary
+    if T == 1:
+        q = wide.as_strided((1, H, D), (wide.stride(0), D, 1))
+        k = wide[:, H * D:H * D + D]
+        assert k.stride(0) % 8
+    else:
+        q = wide[:, :D].contiguous().as_strided((T, 1, D), (D, 3, 1))
+        k = wide[:, D:2 * D].contiguous()
+    freq = _freq(64).cuda()
+    cache = torch.zeros(pg.num_blocks, PAGE, D, dtype=torch.bfloat16, device="cuda")
+    want_c = torch.zeros_like(cache)
+    kw = dict(rope_off=64)
+    want = dsa.dsa_qk_norm_rope(pg.batch(), freq, torch.empty_strided(q.shape, (H * D, D, 1), dtype=q.dtype, device="cuda").copy_(q),
+                                torch.empty_strided(k.shape, (D, 1), dtype=k.dtype, device="cuda").copy_(k), k_cache=want_c, **kw)
+    got = dsa.dsa_qk_norm_rope(pg.batch(), freq, q, k, k_cache=cache, **kw)
+    assert_status_ok()
+    assert torch.equal(got, want) and torch.equal(cache, want_c)
+    same = dsa.dsa_qk_norm_rope(pg.batch(), freq, q, q_out=q, **kw)      # in place
+    assert_status_ok()
+    assert same.data_ptr() == q.data_ptr() and torch.equal(same, want)
+
+
+def test_one_token_of_a_larger_buffer_in_place():
+    pg = Paged([90], [1], seed=7)
+    buf = randn(91, 4, 9, 128).cuda()
+    rest = buf.clone()
+    q = buf[:1, :6]
+    want = dsa.dsa_qk_norm_rope(pg.batch(), _freq(64).cuda(), q.clone().view(1, 6, 128), rope_off=0)
+    dsa.dsa_qk_norm_rope(pg.batch(), _freq(64).cuda(), q, q_out=q, rope_off=0)
+    assert_status_ok()
+    assert torch.equal(buf[:1, :6], want)
+    assert torch.equal(buf[1:], rest[1:]) and torch.equal(buf[0, 6:], rest[0, 6:])
