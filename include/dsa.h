@@ -492,7 +492,8 @@ DSA_API dsa_status dsa_attn_weight(const dsa_batch* batch, const dsa_attn_inputs
  * that any sequence of the batch still reads from here; new pages must be
  * distinct.  batch->cu_q and max_q_per_seq are not used (but checked).
  * A page id out of range is recorded as DSA_ERR_DEVICE_BOUNDS and the row is not
- * copied; a length above max_seq_len likewise, and is taken as max_seq_len.
+ * copied (without arrays no page is looked at); a length above max_seq_len likewise,
+ * and is taken as max_seq_len.
  */
 typedef struct {
     const void* src;            /* device [num_blocks, 64, row_bytes]                                  */

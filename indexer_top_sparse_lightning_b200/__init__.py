@@ -794,7 +794,7 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
         raise ValueError(f"keep {keep} has no room for sink {sink} and recent {recent}")
     if len(arrays) != len(new_arrays):
         raise ValueError(f"{len(arrays)} arrays, {len(new_arrays)} new ones")
-    old_blocks, new_blocks = batch.num_blocks, new_arrays[0].shape[0] if len(new_arrays) else max(1, B * W)
+    old_blocks, new_blocks = batch.num_blocks, new_arrays[0].shape[0] if len(new_arrays) else 1
     copies = (_CacheArray * max(1, len(arrays)))()
     for i, (a, c) in enumerate(zip(arrays, new_arrays)):
         if not isinstance(a, torch.Tensor) or a.dim() < 2:

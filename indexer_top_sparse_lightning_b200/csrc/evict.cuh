@@ -489,12 +489,16 @@ __global__ void __launch_bounds__(kEvictCopyThreads, 6) evict_copy_kernel(const 
         const int j = j0 + (int)threadIdx.x;
         const int pos = __ldcg(p.idx + (int64_t)b * p.keep + j);
         int64_t src = -1, dst = -1;
+        bool bad = true;
         if (pos >= 0 && pos < L) {
-            src = cache_row(p.block_table, p.max_blocks, p.num_blocks, b, pos);
-            dst = cache_row(p.new_table, p.new_max_blocks, p.new_num_blocks, b, j);
+            if (p.n_arrays > 0) {                        // (without arrays no page is looked at)
+                src = cache_row(p.block_table, p.max_blocks, p.num_blocks, b, pos);
+                dst = cache_row(p.new_table, p.new_max_blocks, p.new_num_blocks, b, j);
+            }
+            bad = p.n_arrays > 0 && (src < 0 || dst < 0);
             if (p.new_weight) p.new_weight[(int64_t)b * p.new_stride + j] = __ldg(p.weight + (int64_t)b * p.stride + pos);
         }
-        if (src < 0 || dst < 0) {
+        if (bad) {
             src = -1;
             atomicCAS(p.status, 0u, (uint32_t)kStBounds);
         }

@@ -224,3 +224,18 @@ def test_long_sequences_captured_and_on_two_streams():
                 g.replay()
     assert_status_ok()
     assert all(torch.equal(idx, x) for x in many + [x for _, x in graphs])
+
+
+@pytest.mark.parametrize("L", [300, 70000])
+def test_without_arrays_no_page_is_looked_at(L):
+    # the new weights alone: ids of a larger pool, or of no page at all, are nobody's concern
+    pg = Paged([L], [1], seed=25)
+    w = torch.from_numpy(weights(1, L, 26)).cuda()
+    b, ws = pg.batch(), dsa.Workspace()
+    table = torch.tensor([[7, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")
+    new = torch.full((1, 128), -5.0, device="cuda")
+    idx, _ = dsa.dsa_cache_evict(b, w, 128, table, [], [], new_weight=new, workspace=ws)
+    assert dsa.get_status(ws) == 0
+    want = choose(w[0].cpu().numpy(), L, 128, 0, 0)
+    np.testing.assert_array_equal(idx[0].cpu().numpy(), want)
+    assert torch.equal(new[0].cpu(), w[0].cpu()[torch.from_numpy(want)])
