@@ -790,6 +790,8 @@ def dsa_cache_evict(batch: Batch, weight, keep: int, new_table, arrays, new_arra
     wp = _dense(weight, "weight", torch.float32, (B, n), dev)
     W = new_table.shape[1] if isinstance(new_table, torch.Tensor) and new_table.dim() == 2 else None
     tp = _dense(new_table, "new_table", torch.int32, (B, W), dev)
+    if keep > 0x7FFFFFFF:
+        raise ValueError(f"keep {keep} does not fit 32 bits")
     if keep < 0 or sink < 0 or recent < 0 or sink + recent > keep:
         raise ValueError(f"keep {keep} has no room for sink {sink} and recent {recent}")
     if len(arrays) != len(new_arrays):

@@ -239,3 +239,12 @@ def test_without_arrays_no_page_is_looked_at(L):
     want = choose(w[0].cpu().numpy(), L, 128, 0, 0)
     np.testing.assert_array_equal(idx[0].cpu().numpy(), want)
     assert torch.equal(new[0].cpu(), w[0].cpu()[torch.from_numpy(want)])
+
+
+def test_a_count_that_32_bits_would_wrap_is_refused():
+    pg = Paged([300], [1], seed=27)
+    w, t = torch.zeros(1, 300, device="cuda"), torch.zeros(1, 5, dtype=torch.int32, device="cuda")
+    idx = torch.empty(1, 4, dtype=torch.int32, device="cuda")
+    for keep in (2 ** 32 + 4, 2 ** 31):
+        with pytest.raises(ValueError, match="keep"):
+            dsa.dsa_cache_evict(pg.batch(), w, keep, t, [], [], out_idx=idx)
