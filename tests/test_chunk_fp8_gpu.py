@@ -262,3 +262,67 @@ def test_tiles_of_zeros(n, zero, mag):
     q = (randn(64, pg.T, H, ROW, scale=3.0).float() * 2.0 ** -mag).to(torch.bfloat16)
     out, lse = run(pg, q, codes, kv_scale=scale.cuda())
     check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
+
+
+def _graphs_and_streams(call):
+    """call(**kw) gives the same bits twice, on two streams at once, and from two graphs replayed at once."""
+    ref, rl = call()
+    again, al = call()
+    assert torch.equal(ref, again) and torch.equal(rl, al)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [call(stream=s) for _ in range(4) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = call()
+        graphs.append((g, res))
+    for (g, _), s in zip(graphs, (s1, s2)):
+        with torch.cuda.stream(s):
+            g.replay()
+    assert_status_ok()
+    assert all(torch.equal(o, ref) and torch.equal(x, rl) for o, x in outs + [r for _, r in graphs])
+
+
+def test_repeats_captures_and_streams_agree_where_the_kernel_converts():
+    # fewer (token, head) rows than are worth a copy of the cache
+    pg = Paged([5000, 900, 64, 3000], [3, 60, 1, 7], seed=9)
+    assert int(pg.nq.max()) * 64 < 4096
+    q = randn(17, pg.T, 64, ROW, scale=3.0).cuda()
+    codes, scale, _ = cache(pg, 18)
+    b, codes, scale = pg.batch(), codes.cuda(), scale.cuda()
+    _graphs_and_streams(lambda **kw: dsa.dsa_chunk_attn(b, q, codes, SCALE, kv_scale=scale, **kw))
+
+
+def test_growing_scores_where_the_kernel_converts():
+    pg = Paged([1500], [31], seed=3)
+    q = randn(5, pg.T, 128, ROW).abs()
+    x = randn(6, pg.num_blocks, PAGE, ROW)
+    x.view(-1, ROW)[pg.rows(0)] = (randn(7, 1500, ROW).float() * 0.5 + torch.linspace(-2, 2, 1500)[:, None]).to(torch.bfloat16)
+    codes, scale, val = fp8_rows(x)
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    check(pg, out, lse, reference(pg, q, lambda b: val.view(-1, ROW)[pg.rows(b)], fp16=True))
+
+
+@pytest.mark.parametrize("what", ["codes", "scales"])
+def test_later_tokens_rows_do_not_reach_earlier_ones_where_the_kernel_converts(what):
+    n, good, H = 30, 20, 128
+    pg = Paged([400], [n], seed=4)
+    q = randn(8, n, H, ROW, scale=3.0)
+    codes, scale, val = cache(pg, 9)
+    rows = pg.rows(0)
+    late = rows[400 - n + good:]
+    if what == "codes":
+        codes.view(-1, ROW)[late, 100] = NAN
+    else:
+        # (of every tile in turn, the two that share an accumulator among them)
+        scale.view(-1, 5)[late, np.arange(n - good) % 5] = math.nan
+    clean = val.clone()
+    clean[late] = 0
+    out, lse = run(pg, q, codes, kv_scale=scale.cuda())
+    ro, rl, bo, bl = reference(pg, q, lambda b: clean[rows], fp16=True)
+    assert ((out[:good].double() - ro[:good]).abs() <= bo[:good]).all()
+    assert ((lse[:good].double() - rl[:good]).abs() <= bl[:good]).all()
+    assert not torch.isfinite(lse[good:]).any()

@@ -258,3 +258,74 @@ def test_more_new_tokens_than_rows_are_reported():
     lse[n:] = -math.inf                                  # rows that are not there add nothing
     val, bound = expect(pg, q, lambda b: kv.view(-1, ROW)[pg.rows(b)], lse, torch.zeros(3, 400), 1.0)
     assert ((w.double() - val).abs() <= bound).all()
+
+
+def _codes(pg, seed):
+    """(codes, scales, values): NaN codes, and scales NaN, infinite or huge, where nobody looks."""
+    codes, scale, val = fp8_rows(randn(seed, pg.num_blocks, PAGE, ROW))
+    used = np.zeros(pg.num_blocks * PAGE, bool)
+    for b in range(pg.B):
+        used[pg.rows(b)] = True
+    codes.view(-1, ROW)[~used] = 0x7F
+    scale.view(-1, 5)[~used] = torch.tensor([math.nan, math.inf, -math.inf, 3e38, -0.0])
+    return codes, scale, val.view(-1, ROW)
+
+
+@pytest.mark.parametrize("lens,nq,H,decay", SHAPES)
+def test_formula_over_an_fp8_cache(lens, nq, H, decay):
+    pg = Paged(lens, nq, seed=H, pad=2)
+    q = randn(1 + H, pg.T, H, ROW, scale=3.0)
+    codes, scale, val8 = _codes(pg, 2)
+    cd, sd = codes.cuda(), scale.cuda()
+    _, lse = dsa.dsa_chunk_attn(pg.batch(), q.cuda(), cd, SCALE, kv_scale=sd)
+    w0 = torch.rand(pg.B, max(lens) + 5, generator=torch.Generator().manual_seed(3)) * 4
+    w = w0.cuda()
+    dsa.dsa_attn_weight(pg.batch(), q.cuda(), cd, SCALE, lse, w, decay=decay, kv_scale=sd)
+    assert_status_ok()
+    val, bound = expect(pg, q, lambda b: val8[pg.rows(b)], lse, w0, decay, fp8=True)
+    for b in range(pg.B):
+        L = int(pg.lens[b]) if pg.nq[b] else 0     # beyond: untouched
+        assert torch.equal(w[b, L:].cpu(), w0[b, L:])
+        assert ((w[b, :L].double() - val[b, :L]).abs() <= bound[b, :L]).all()
+
+
+def test_bad_page_of_an_fp8_cache_is_reported():
+    pg = Paged([600, 500], [1, 9], seed=7)
+    q = randn(61, pg.T, 32, ROW, scale=3.0)
+    codes, scale, val8 = _codes(pg, 62)
+    _, lse = dsa.dsa_chunk_attn(pg.batch(), q.cuda(), codes.cuda(), SCALE, kv_scale=scale.cuda())
+    rows = [val8[pg.rows(b)] for b in range(2)]
+    pg.table[1, 3] = -5
+    ws, w = dsa.Workspace(), torch.zeros(2, 600, device="cuda")
+    dsa.dsa_attn_weight(pg.batch(), q.cuda(), codes.cuda(), SCALE, lse, w, kv_scale=scale.cuda(), workspace=ws)
+    assert dsa.get_status(ws) == 6
+    val, bound = expect(pg, q, lambda b: rows[b], lse, torch.zeros(2, 600), 1.0, fp8=True,
+                        hidden=lambda b: (torch.arange(int(pg.lens[b])) // PAGE == 3) & (b == 1))
+    assert ((w.double() - val).abs() <= bound).all()
+
+
+def test_repeats_streams_and_captures_agree_over_an_fp8_cache():
+    pg = Paged([5000, 900, 64, 3000], [3, 200, 1, 7], seed=9)
+    q = randn(71, pg.T, 64, ROW, scale=3.0).cuda()
+    codes, scale, _ = _codes(pg, 72)
+    codes, scale, b = codes.cuda(), scale.cuda(), pg.batch()
+    _, lse = dsa.dsa_chunk_attn(b, q, codes, SCALE, kv_scale=scale)
+    call = lambda w, **kw: dsa.dsa_attn_weight(b, q, codes, SCALE, lse, w, kv_scale=scale, **kw)  # noqa: E731
+    ref = call(torch.zeros(4, 5000, device="cuda"))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ws = [torch.zeros(4, 5000, device="cuda") for _ in range(6)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        call(ws[i], stream=(s1, s2)[i % 2])
+    torch.cuda.synchronize()
+    graphs = []
+    for i in (4, 5):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(ws[i], decay=0.0)
+        graphs.append(g)
+    for g, s in zip(graphs, (s1, s2)):
+        with torch.cuda.stream(s):
+            g.replay()
+    assert_status_ok()
+    assert all(torch.equal(w, ref) for w in ws)
