@@ -415,10 +415,11 @@ DSA_API dsa_status dsa_qk_norm_rope(const dsa_batch* batch, const dsa_rope_input
  * RoPE elements take part as two fp16 values each: to 2^-21 of themselves or 2^-31 of the
  * scale before theirs, whichever is more; where their scale is more than 2^22 times that
  * one, the elements before them are rounded to 2^-31 of theirs), and the output's values
- * are rounded to fp16.  Where max_q_per_seq new
- * tokens make 4096 (token, head) rows or more, and batch x max_seq_len positions no
- * more than 96 MiB of fp16 copy, the cache is copied into the scratch once (2304 bytes a
- * position: two fp16 values per element and a factor per page, to 2^-22 of a value).
+ * are rounded to fp16.  Where max_q_per_seq new tokens make 4096 (token, head) rows or
+ * more, and batch x max_seq_len positions no more than 96 MiB of fp16 copy, the cache is copied into the scratch once (2304 bytes a
+ * position: two fp16 values per element and a factor per page, to 2^-22 of a value or
+ * 2^-29 of its page's largest scale, whichever is more).  Scales of a sequence that lie more
+ * than 2^16 apart cost the small ones bits (a tile of zeros has the scale 1).
  * out device [T, H, 512] bf16; lse device [T, H] fp32 (natural log) or NULL.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * bf16 (fp16 over an FP8 cache) for the second product.
@@ -461,8 +462,10 @@ DSA_API dsa_status dsa_chunk_attn(const dsa_batch* batch, const dsa_attn_inputs*
  * q, cache formats, block tables, status and the bounds reported there are those
  * of dsa_chunk_attn; positions of a page whose id is out of range add nothing.  An
  * FP8 cache is copied into the scratch as fp16 (two values per element and a
- * power-of-two factor per page: 2^-22 of a value), which then holds max_seq_len
- * rows of 2304 bytes for each sequence.
+ * power-of-two factor per page: 2^-22 of a value, or 2^-29 of the page's largest scale),
+ * which then holds max_seq_len rows of 2304 bytes for each sequence.
+ * A score is one fp32 sum of 576 products on the tensor core, which leaves weights off by
+ * up to 5e-6 of themselves.
  * More than max_q_per_seq new tokens of a sequence, or a length above max_seq_len,
  * are recorded as DSA_ERR_DEVICE_BOUNDS (the surplus is not counted); so is a
  * length below the count of new tokens (tokens at p_t < 0 add nothing).

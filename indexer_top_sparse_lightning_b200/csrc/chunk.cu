@@ -16,10 +16,12 @@ using namespace dsa::host;
 namespace {
 
 // An FP8 cache is copied as fp16 once per call, rather than converted in the kernel, when a
-// sequence can have this many tiles and the copy stays in L2.  (Us, copy / kernel, 128 heads:
-// one sequence of 16K positions with 16 new tokens 177 / 178, 64 456 / 572, 512 2857 / 4132, 2048
-// 10894 / 15592; 8 sequences of 16K to 131K, whose copy is 1.2 GB, 64 tokens 17864 / 16706, 2
-// tokens 899 / 548.)
+// sequence can have this many tiles and the copy is no larger than kCopyBytes, which bounds the
+// scratch that a call needs beside its cache.  (Us, copy / kernel, 128 heads: one sequence of 16K
+// positions with 16 new tokens 177 / 178, 64 456 / 572, 512 2857 / 4132, 2048 10894 / 15592; 8 sequences of
+// 16K to 131K, whose copy is 1.2 GB, 64 tokens 17864 / 16706, 2 tokens 899 / 548.  One sequence
+// past the bound: 2048 tokens over 48K positions 36.0 / 44.1 ms, 64K 48.5 / 58.9, 128K 98.6 / 120.1; over
+// 64K 512 tokens 12.8 / 14.9, 256 6.7 / 7.5, 64 2.0 / 2.5: there the bound costs a fifth.)
 constexpr int64_t kCopyTiles = 32;
 constexpr int64_t kCopyBytes = int64_t(96) << 20;
 

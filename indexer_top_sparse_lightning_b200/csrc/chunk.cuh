@@ -38,9 +38,10 @@
 // L2 (each CTA needs its page whole, and its half of the value columns of both):
 // at chunk lengths the L2 path and the MMAs are about even, and a decode step
 // of 128 heads sits at the ridge of HBM and tensor rate.  The last 2048 tokens of a
-// 16K prompt take 7.15 ms, 1.22 PFLOP/s (cuBLAS holds 1.38 for as long; the clock is at the power
-// limit); 32 tokens over 32K positions each 340 us, 3.6 TB/s and 0.86 PFLOP/s at once;
-// one token at 4K 16.6 us, most of it start, planning and merge.
+// 16K prompt take 7.15 to 7.35 ms, 1.19 to 1.22 PFLOP/s (cuBLAS holds 1.38 for as long; the clock is
+// at the power limit); 32 tokens over 32K positions each 340 to 370 us, 3.3 to 3.6 TB/s and 0.79
+// to 0.86 PFLOP/s at once (at 1.30 GHz when the calls go on for seconds; the merge ends 21 us after
+// the attention), of 16 heads 290; one token at 4K 16.6 us, most of it start, planning and merge.
 //
 // Masked positions.  Scores past a row's own position are replaced, not
 // multiplied.  In P.V a weight of zero still multiplies the value row, so rows

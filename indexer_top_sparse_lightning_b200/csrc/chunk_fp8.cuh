@@ -1,13 +1,14 @@
 // chunk_fp8.cuh -- the operand side of dense attention over an FP8 latent cache:
 // codes from global memory to the fp16 operands of the MMAs in shared memory.
 //
-// What bounds it: instructions and shared memory.  A block's 70 KB of codes per CTA become 144
-// KB of operands; the converting and softmax warps issue in 61 % of the cycles and the
-// shared-memory pipe is half busy with them, beside the MMAs' own reads (tensor pipes 24 %).
-// Two tokens of 8 sequences of 16K to 128K positions take 524 us, two tiles of 128 rows
-// over 530K positions; over an fp16 copy of the cache in global memory, which wrote and
-// read 2304 bytes a position, they took 900 with the copy.  (Many tiles over positions whose copy
-// stays in L2 take the copy: chunk.cu.)
+// What bounds it is no single unit.  Two tokens of 8 sequences of 16K to 128K positions, two tiles of
+// 128 rows over 530K positions, take 524 to 551 us.  Of a block's 7830 cycles the issue slots are
+// busy in 0.53, the shared-memory pipe in 0.50 with loads and stores (3950 wavefronts a block:
+// 1590 loads, 1650 stores, a fifth of them bank conflicts, and barriers) and in 0.26 with the operand
+// reads of the MMAs (2020), the tensor pipes in 0.29, and HBM gives 1.1 TB/s.  Most stalls are fixed
+// latencies, barriers and branches, then shared memory and instructions that are not there yet.  Over
+// an fp16 copy of the cache in global memory, which wrote and read 2304 bytes a position, they
+// took 900 us with the copy.  (Many tiles over few positions take the copy: chunk.cu.)
 //
 // Two teams of CONV_WARPS warps convert, one the keys and one the values, a ring group
 // (16 KB of fp16, 8 KB of codes) at a time; the codes of the groups behind are on their way to

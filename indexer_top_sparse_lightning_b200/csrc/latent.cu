@@ -14,7 +14,8 @@
 namespace dsa {
 
 // The pages of every sequence as fp16: x = code x tile scale / page factor, rounded
-// (2^-11 of the value), and the rest x - that, rounded (2^-22), in a copy that is laid out by sequence: page i of
+// (2^-11 of the value), and the rest x - that, rounded (2^-22 of the value, or 2^-29 of the page's largest
+// scale where that is more: fp16's smallest step), in a copy that is laid out by sequence: page i of
 // sequence b at b * pages + i.  The page factor is the power of two that brings the
 // largest value that the page's scales allow below 2^14; positions behind the
 // sequence's end do not count, whatever they hold.  One block per page: its 64 rows

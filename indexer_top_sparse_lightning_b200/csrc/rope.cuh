@@ -9,8 +9,9 @@
 //
 // What bounds it: memory.  Each row is read once and written once (D * 2 bytes
 // each way); the arithmetic is a few operations per element.  8192 tokens of 128 heads of
-// 576 with their keys take 462 us, 5.27 TB/s of the 6.56 of a plain copy.  A decode step
-// is bound by the call: 32 tokens take 7 us on the device, 12.6 with the host's work.  (The launch
+// 576 with their keys take 462 to 471 us, 5.2 TB/s of the 6.56 of a plain copy (three blocks per SM, at
+// 80 registers, spill 40 bytes; four were slower).  A decode step
+// is bound by the call: 32 tokens take 7 us on the device, 11.8 with the host's work.  (The launch
 // is a programmatic dependent, so that it is ready when the kernel before ends: 1000 ragged tokens
 // of 64 heads in a row 15.6 -> 13.4 us.)
 //

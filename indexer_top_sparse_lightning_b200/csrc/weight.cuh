@@ -23,9 +23,11 @@
 //
 // What bounds it: a decode step reads every latent row once (HBM); chunks are bound
 // by the MMAs, 2 * 576 * NR operations per position and tile, with one exponential
-// per (row, position) under them.  32 tokens over 32K positions each take 235 us, 5.2 TB/s of
+// per (row, position) under them.  32 tokens over 32K positions each take 227 to 240 us, 5.2 TB/s of
 // the 6.56 of a plain copy; chunks of 150 to 300 tokens of 64 heads over 5K to 9K positions
-// 268 us, 1.13 PFLOP/s.
+// 268 to 272 us, 1.13 PFLOP/s.  Over an FP8 cache both read an fp16 copy of the rows that the call makes
+// first (596 bytes a position read, 2304 written and read again, and twice the MMAs for the two
+// values of an element): 1190 and 580 us.
 //
 // Roles per CTA (352 threads): warps 0-7 exponentials and sums (lane L of the
 // quarter <-> position 128c + L of the block); warp 8 TMEM allocation, in CTA 0 the
